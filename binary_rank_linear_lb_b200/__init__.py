@@ -15,7 +15,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import List, Optional, Sequence
+from contextlib import ExitStack
+from typing import List, NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -62,7 +63,8 @@ EXPORTS = ("lb_status_string", "lb_version", "lb_pack_signs", "lb_linear_forward
            "lb_workspace_status", "lb_stack_output", "lb_linear_forward_noalloc",
            "lb_noalloc_scratch_bytes", "lb_pack_signs_sliced", "lb_packed_words",
            "lb_stack_plan_host", "lb_linear_forward_xor", "lb_linear_xor_workspace_size",
-           "lb_dual_svid", "lb_dual_svid_workspace_size")
+           "lb_dual_svid", "lb_dual_svid_workspace_size", "lb_quantize_rows",
+           "lb_rmsnorm_quantize", "lb_linear_int8", "lb_token_logprobs")
 
 _lib = None
 
@@ -120,6 +122,16 @@ def lib() -> ctypes.CDLL:
         L.lb_dual_svid.restype = st
         L.lb_dual_svid_workspace_size.argtypes = [i64, i64, i64, ctypes.c_int]
         L.lb_dual_svid_workspace_size.restype = sz
+        L.lb_quantize_rows.argtypes = [vp, st, i64, i64, i64, vp, i64, vp, vp]
+        L.lb_quantize_rows.restype = st
+        L.lb_rmsnorm_quantize.argtypes = [vp, st, i64, i64, i64, vp, i64, vp, i64, vp, st,
+                                          ctypes.c_float, vp, i64, vp, vp]
+        L.lb_rmsnorm_quantize.restype = st
+        L.lb_linear_int8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, st, i64, vp]
+        L.lb_linear_int8.restype = st
+        L.lb_token_logprobs.argtypes = [vp, st, i64, i64, i64, vp, vp, vp, ctypes.c_int, vp, vp,
+                                        vp]
+        L.lb_token_logprobs.restype = st
         _lib = L
     return _lib
 
@@ -338,6 +350,204 @@ def dual_svid(W: torch.Tensor, r: int, n_branches: int = 2, layout: int = LB_LAY
 
 def workspace_status(workspace: torch.Tensor, stream=None) -> int:
     return int(lib().lb_workspace_status(_ptr(workspace), _stream(stream)))
+
+
+# ------------------------------------------------------------------ dense path
+def _scope(stream, *tensors: Optional[torch.Tensor]) -> ExitStack:
+    """Checks that the tensors share one GPU and enters it, and the given stream.
+
+    Outputs allocated inside belong to that stream; inputs used on a stream other than
+    the current one are marked as in use there, so that their memory is not handed out
+    again before the call has run.
+    """
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device != dev):
+            raise ValueError(f"all tensors must be on one CUDA device, got {t.device} and {dev}")
+    scope = ExitStack()
+    if dev.index != torch.cuda.current_device():
+        scope.enter_context(torch.cuda.device(dev))
+    if stream is not None:
+        s = stream if hasattr(stream, "cuda_stream") else \
+            torch.cuda.ExternalStream(int(stream), device=dev)
+        if s.device != dev:
+            raise ValueError(f"stream on {s.device}, tensors on {dev}")
+        if s.cuda_stream != torch.cuda.current_stream().cuda_stream:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+            scope.enter_context(torch.cuda.stream(s))
+    return scope
+
+
+def _rows(t: torch.Tensor, what: str) -> Tuple[int, int, int]:
+    """(rows, columns, row pitch) of a matrix whose rows are contiguous."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must be a matrix with unit stride along its columns")
+    rows, cols = t.shape
+    return rows, cols, t.stride(0) if rows > 1 else max(cols, t.stride(0))
+
+
+def _dtype(t: torch.dtype, what: str) -> int:
+    dt = _DTYPES.get(t)
+    if dt is None:
+        raise ValueError(f"unsupported {what} dtype {t}")
+    return dt
+
+
+def _vector(t: torch.Tensor, n: int, dtype: Optional[torch.dtype], what: str) -> None:
+    if t.dim() != 1 or t.shape[0] != n or (t.stride(0) != 1 and n > 1) or \
+            (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be a contiguous vector of {n}"
+                         + (f" {dtype}" if dtype is not None else "") + " elements")
+
+
+def _codes_out(q, scale, rows: int, cols: int, dev):
+    if q is None:
+        # a pitch of whole 16-byte pieces, which linear_int8's fast kernels read
+        q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :cols]
+    elif q.dtype != torch.int8 or tuple(q.shape) != (rows, cols):
+        raise ValueError(f"q must be an int8 matrix of {rows} x {cols}")
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _vector(scale, rows, torch.float32, "scale")
+    return q, scale
+
+
+def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """lb_quantize_rows: (q int8, scale fp32 per row) of a matrix (rows x cols).
+
+    Used for head weights (a scale per output channel) and for activations (a scale per
+    token).  A new q is a view whose pitch is a multiple of 16 bytes.
+    """
+    rows, cols, ldx = _rows(x, "x")
+    dt = _dtype(x.dtype, "x")
+    with _scope(stream, x, q, scale):
+        q, scale = _codes_out(q, scale, rows, cols, x.device)
+        _check(lib().lb_quantize_rows(_ptr(x), dt, rows, cols, ldx, _ptr(q), _rows(q, "q")[2],
+                                      _ptr(scale), _stream(None)), "lb_quantize_rows")
+    return q, scale
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                     residual: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                     sum_out: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                     scale: Optional[torch.Tensor] = None, stream=None
+                     ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """lb_rmsnorm_quantize: (q, scale, s) with s = x + residual (None without a residual)
+    and scale * q the RMS norm of s (times weight) in 8-bit codes, one scale per row.
+
+    ``sum_out`` receives s; it may be ``residual`` or ``x`` itself.
+    """
+    rows, cols, ldx = _rows(x, "x")
+    dt = _dtype(x.dtype, "x")
+    wdt = LB_F32
+    if weight is not None:
+        _vector(weight, cols, None, "weight")
+        wdt = _dtype(weight.dtype, "weight")
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    for t, what in ((residual, "residual"), (sum_out, "sum_out")):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
+            raise ValueError(f"{what} must have x's shape and dtype")
+    with _scope(stream, x, weight, residual, sum_out, q, scale):
+        q, scale = _codes_out(q, scale, rows, cols, x.device)
+        if residual is not None and sum_out is None:
+            sum_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        ldr = _rows(residual, "residual")[2] if residual is not None else 0
+        lds = _rows(sum_out, "sum_out")[2] if residual is not None else 0
+        _check(lib().lb_rmsnorm_quantize(_ptr(x), dt, rows, cols, ldx, _ptr(residual), ldr,
+                                         _ptr(sum_out), lds, _ptr(weight), wdt, float(eps),
+                                         _ptr(q), _rows(q, "q")[2], _ptr(scale), _stream(None)),
+               "lb_rmsnorm_quantize")
+    return q, scale, sum_out
+
+
+def linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                y: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
+                stream=None) -> torch.Tensor:
+    """lb_linear_int8: y (M x out) = xs[:, None] * ws[None, :] * (xq @ wq.T), summed exactly.
+
+    ``xq`` (M x in) and ``wq`` (out x in) are int8 codes with fp32 scales per row, as
+    quantize_rows and rmsnorm_quantize give them; ``dtype`` is that of a new y.
+    """
+    M, k, ldx = _rows(xq, "xq")
+    n, kw, ldw = _rows(wq, "wq")
+    if xq.dtype != torch.int8 or wq.dtype != torch.int8 or k != kw:
+        raise ValueError("xq and wq must be int8 matrices with the same number of columns")
+    _vector(xs, M, torch.float32, "xs")
+    _vector(ws, n, torch.float32, "ws")
+    if y is not None and tuple(y.shape) != (M, n):
+        raise ValueError(f"y must be {M} x {n}")
+    with _scope(stream, xq, xs, wq, ws, y):
+        if y is None:
+            y = torch.empty((M, n), dtype=dtype, device=xq.device)
+        _check(lib().lb_linear_int8(_ptr(xq), ldx, _ptr(xs), M, _ptr(wq), ldw, _ptr(ws), k, n,
+                                    _ptr(y), _dtype(y.dtype, "y"), _rows(y, "y")[2],
+                                    _stream(None)), "lb_linear_int8")
+    return y
+
+
+class TokenLogprobs(NamedTuple):
+    """token_logprobs' results: per row the given token's log probability (None without
+    tokens), the entropy, and the ids and log probabilities of the alternatives."""
+    logprob: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    top_id: Optional[torch.Tensor]
+    top_logprob: Optional[torch.Tensor]
+
+
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, top: int = 0,
+                   stream=None) -> TokenLogprobs:
+    """lb_token_logprobs: log probabilities of ``tokens`` (int64, one per row; negative:
+    none), entropy and the ``top`` (0 .. 32) most likely alternatives of logits
+    (rows x vocab; -inf masks a token)."""
+    rows, vocab, ld = _rows(logits, "logits")
+    dt = _dtype(logits.dtype, "logits")
+    if tokens is not None:
+        _vector(tokens, rows, torch.int64, "tokens")
+    top = int(top)
+    if not 0 <= top <= min(32, vocab):
+        raise ValueError(f"top must be 0 .. {min(32, vocab)}")
+    with _scope(stream, logits, tokens):
+        new = lambda shape, t: torch.empty(shape, dtype=t, device=logits.device)
+        logprob = new(rows, torch.float32) if tokens is not None else None
+        entropy = new(rows, torch.float32)
+        top_id = new((rows, top), torch.int64) if top else None
+        top_lp = new((rows, top), torch.float32) if top else None
+        _check(lib().lb_token_logprobs(_ptr(logits), dt, rows, vocab, ld, _ptr(tokens),
+                                       _ptr(logprob), _ptr(entropy), top, _ptr(top_id),
+                                       _ptr(top_lp), _stream(None)), "lb_token_logprobs")
+    return TokenLogprobs(logprob, entropy, top_id, top_lp)
+
+
+class Head:
+    """What follows a stack: the final norm and an output head in 8-bit integers.
+
+    ``wq`` (vocab x hidden, int8) and ``ws`` (fp32 [vocab]) are the head's codes and
+    channel scales (quantize_rows of the dense head), ``norm_weight`` the final norm's
+    weight or None for the stacks' weightless norm.
+    """
+
+    def __init__(self, wq: torch.Tensor, ws: torch.Tensor,
+                 norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-5):
+        self.wq, self.ws, self.norm_weight, self.eps = wq, ws, norm_weight, eps
+        self.vocab, self.hidden = wq.shape
+
+    def logits(self, h: torch.Tensor, dtype: torch.dtype = torch.float32,
+               stream=None) -> torch.Tensor:
+        """Logits (tokens x vocab) of residual streams h (tokens x hidden, or one token's)."""
+        h2 = h if h.dim() == 2 else h.reshape(1, -1)
+        xq, xs, _ = rmsnorm_quantize(h2, self.norm_weight, eps=self.eps, stream=stream)
+        return linear_int8(xq, xs, self.wq, self.ws, dtype=dtype, stream=stream)
+
+    def logprobs(self, h: torch.Tensor, tokens: Optional[torch.Tensor] = None, top: int = 0,
+                 stream=None) -> TokenLogprobs:
+        """Log probabilities of ``tokens``, entropy and alternatives after h (see token_logprobs)."""
+        return token_logprobs(self.logits(h, stream=stream), tokens, top, stream)
 
 
 # ------------------------------------------------------------------ stacks

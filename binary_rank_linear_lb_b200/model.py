@@ -18,7 +18,8 @@ from typing import List, Optional
 
 import torch
 
-from . import LB_LAYOUT_ROWS, LB_LAYOUT_SLICES, Branch, Stack, pack_signs, slice_words, synth
+from . import (LB_LAYOUT_ROWS, LB_LAYOUT_SLICES, Branch, Head, Stack, pack_signs, quantize_rows,
+               slice_words, synth)
 from .configs import Model, proj_shape
 
 
@@ -99,3 +100,14 @@ def build_mlp_block(model: Model, bpw: float, base: int = 0, n_branches: int = 2
         i, o = proj_shape(p, model.hidden, model.inter, model.kv_dim)
         L[p] = build_linear(i, o, rk[p], base, 0, p, n_branches, device, signs, layout=layout)
     return Stack([L], [list(rk)], model.hidden, model.inter, mlp_only=True, device=device)
+
+
+def build_head(model: Model, base: int = 0, vocab: int = 32000, device="cuda",
+               norm_weight: bool = True) -> Head:
+    """The head after a stack: a dense fp16 weight (vocab x hidden, N(0, 1 / hidden)) drawn
+    from its seed and quantised to 8 bits per channel, and a final norm weight |N(1, 0.1)|."""
+    s = lambda k: synth.tensor_seed(base, model.n_layers, 0, 0, k)
+    w = synth.latent(vocab, model.hidden, s(synth.KIND_HEAD), device)
+    wq, ws = quantize_rows((w * model.hidden ** -0.5).to(torch.float16))
+    nw = synth.scale(model.hidden, s(synth.KIND_NORM), device) if norm_weight else None
+    return Head(wq, ws, nw)

@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import torch
 
-KIND_U, KIND_V, KIND_H, KIND_G, KIND_L, KIND_X = range(6)
+KIND_U, KIND_V, KIND_H, KIND_G, KIND_L, KIND_X, KIND_HEAD, KIND_NORM = range(8)
 
 
 def tensor_seed(base: int, layer: int, proj: int, branch: int, kind: int) -> int:

@@ -271,6 +271,104 @@ size_t lb_noalloc_scratch_bytes(void);
 int lb_linear_path(int64_t M, int64_t in, int64_t out, int64_t r);
 
 /*
+ * The dense path.  Only the linears of the transformer blocks are factorised;
+ * the final norm, the output head and what is read from its logits are dense.
+ * The four calls below cover that path in 8-bit integers: rows are quantised
+ * (with the RMS norm in front, or on their own), multiplied with 8-bit weights,
+ * and the logits turned into log probabilities.  Common to the four:
+ *   - every matrix is row-major with a row pitch ld* in elements, at least its
+ *     columns; pointers need only the alignment of their element type.  Pitches
+ *     and pointers that are multiples of 16 bytes are read in wide pieces, others
+ *     by narrower loads, with the same results;
+ *   - no workspace: a call keeps nothing, so calls on several streams, and
+ *     captured graphs that are replayed together, share nothing;
+ *   - bytes between the columns and the pitch are neither read nor written;
+ *   - outputs overlap neither inputs nor one another, except where stated;
+ *   - sizes of zero are refused (LB_ERR_INVALID_ARG).
+ */
+
+/*
+ * lb_quantize_rows — 8-bit codes with one scale per row.
+ *   x      : device, rows x cols, dtype x_dtype, pitch ldx
+ *   q      : device int8, rows x cols, pitch ldq, written: with peak = max|x_i|
+ *            of the row, q_i = rint(127 x_i / peak) of the exact quotient, ties to
+ *            even, so -127 <= q_i <= 127
+ *   scale  : device fp32 [rows], written: peak / 127
+ * scale * q_i is within half a step of x_i.  A row of zeros has scale 0.  A row
+ * with a NaN or an infinity has scale NaN and codes 0, so that what is computed
+ * from it is NaN.  Errors: LB_ERR_INVALID_ARG (null pointer, rows or cols <= 0,
+ * rows > 2^31 - 1, cols > 2^24, a pitch below cols or above 2^40, bad dtype),
+ * LB_ERR_ALIGNMENT, LB_ERR_UNSUPPORTED, LB_ERR_CUDA.
+ */
+lb_status lb_quantize_rows(const void *x, lb_dtype x_dtype, int64_t rows, int64_t cols,
+                           int64_t ldx, int8_t *q, int64_t ldq, float *scale, void *stream);
+
+/*
+ * lb_rmsnorm_quantize — the residual's addition, the RMS norm and the 8-bit
+ * codes of its result in one pass.  Per row:
+ *   s     = x + residual, rounded to x_dtype (s = x without a residual),
+ *   n_i   = s_i w_i / sqrt(mean(s^2) + eps),
+ *   scale = max|n_i| / 127,  q_i = rint(n_i / scale) of the exact quotient.
+ * The norm is taken of s as it is stored, so it can be recomputed from `sum`.
+ *   x, residual : device, rows x cols of x_dtype, pitches ldx and ldr; residual
+ *                 may be NULL (then sum must be NULL too, and ldr, lds are ignored)
+ *   sum         : device, rows x cols of x_dtype, pitch lds, written: s.  May be
+ *                 residual or x itself (same pointer, same pitch)
+ *   weight      : device [cols] of weight_dtype, or NULL for ones (the stacks' norm)
+ *   eps         : >= 0 (the stacks use 1e-5)
+ *   q, scale    : as lb_quantize_rows, zero and non-finite rows included (non-finite
+ *                 products s_i w_i of the exact values count)
+ * Errors: as lb_quantize_rows.
+ */
+lb_status lb_rmsnorm_quantize(const void *x, lb_dtype x_dtype, int64_t rows, int64_t cols,
+                              int64_t ldx, const void *residual, int64_t ldr, void *sum,
+                              int64_t lds, const void *weight, lb_dtype weight_dtype, float eps,
+                              int8_t *q, int64_t ldq, float *scale, void *stream);
+
+/*
+ * lb_linear_int8 — a dense linear in 8-bit integers with a scale per token and
+ * per output channel:
+ *   y[m, n] = xs[m] * ws[n] * sum_k xq[m, k] * wq[n, k]
+ *   xq, xs : device int8 M x in (pitch ldx) and fp32 [M]
+ *   wq, ws : device int8 out x in (pitch ldw) and fp32 [out]
+ *   y      : device M x out of y_dtype (LB_F32, LB_F16 or LB_BF16), pitch ldy, written
+ * The sum is exact; (sum rounded to fp32) * xs * ws is rounded at each product
+ * and then to y_dtype.  -128 is an ordinary code.  The fast kernels read xq and wq in 16-byte
+ * pieces (pointers and pitches multiples of 16); other calls run a slower one.
+ * Errors: LB_ERR_INVALID_ARG (null pointer, M, in or out <= 0, M or out > 2^24,
+ * in > 131071 (the sum has to fit 32 bits), a pitch below its columns or above
+ * 2^32, bad dtype), LB_ERR_ALIGNMENT, LB_ERR_UNSUPPORTED, LB_ERR_CUDA.
+ */
+lb_status lb_linear_int8(const int8_t *xq, int64_t ldx, const float *xs, int64_t M,
+                         const int8_t *wq, int64_t ldw, const float *ws, int64_t in, int64_t out,
+                         void *y, lb_dtype y_dtype, int64_t ldy, void *stream);
+
+/*
+ * lb_token_logprobs — what is read from logits: log probabilities of given
+ * tokens, the entropy, and the most likely alternatives, without storing the
+ * distribution.  Per row x, with log p = x - log sum e^x (natural logarithm):
+ *   logits      : device, rows x vocab, dtype, pitch ld; -inf masks a token
+ *   tokens      : device int64 [rows], or NULL: one token per row.  A negative one
+ *                 stands for "none" and gets 0; one >= vocab gets NaN
+ *   logprob     : device fp32 [rows], written: log p of the token (NULL with tokens)
+ *   entropy     : device fp32 [rows], written: -sum p log p, or NULL
+ *   top         : 0 .. 32 alternatives per row (at most vocab)
+ *   top_id      : device int64 [rows][top], written: the tokens of the largest logits,
+ *                 in falling order, equal ones by rising token
+ *   top_logprob : device fp32 [rows][top], written: their log p
+ * (top_id and top_logprob may be NULL with top = 0.)  A row whose logits are
+ * all -inf has no distribution: its log probabilities are -inf and its entropy 0.
+ * A row with a NaN or +inf has NaN log probabilities and entropy (its
+ * alternatives: NaN before everything, by rising token).  Errors:
+ * LB_ERR_INVALID_ARG (null pointers, nothing asked for, rows <= 0 or > 2^31 - 1,
+ * vocab <= 0 or > 2^24, ld below vocab or above 2^40, bad top or dtype),
+ * LB_ERR_ALIGNMENT, LB_ERR_UNSUPPORTED, LB_ERR_CUDA.
+ */
+lb_status lb_token_logprobs(const void *logits, lb_dtype dtype, int64_t rows, int64_t vocab,
+                            int64_t ld, const int64_t *tokens, float *logprob, float *entropy,
+                            int top, int64_t *top_id, float *top_logprob, void *stream);
+
+/*
  * Decoder stacks.  A stack runs, for one token (batch 1), the linears of
  * n_layers Llama-2-shaped decoder layers and the glue between them:
  *
