@@ -333,11 +333,12 @@ lb_status lb_rmsnorm_quantize(const void *x, lb_dtype x_dtype, int64_t rows, int
  *   wq, ws : device int8 out x in (pitch ldw) and fp32 [out]
  *   y      : device M x out of y_dtype (LB_F32, LB_F16 or LB_BF16), pitch ldy, written
  * The sum is exact; (sum rounded to fp32) * xs * ws is rounded at each product
- * and then to y_dtype.  -128 is an ordinary code.  The fast kernels read xq and wq in 16-byte
+ * and then to y_dtype.  -128 is an ordinary code.  A device-side wait that gives
+ * up (about 2 s) leaves NaN in the outputs it held up.  The fast kernels read xq and wq in 16-byte
  * pieces (pointers and pitches multiples of 16); other calls run a slower one.
  * Errors: LB_ERR_INVALID_ARG (null pointer, M, in or out <= 0, M or out > 2^24,
- * in > 131071 (the sum has to fit 32 bits), a pitch below its columns or above
- * 2^32, bad dtype), LB_ERR_ALIGNMENT, LB_ERR_UNSUPPORTED, LB_ERR_CUDA.
+ * M * out > 2^40, in > 131071 (the sum has to fit 32 bits), a pitch below its
+ * columns or above 2^32, bad dtype), LB_ERR_ALIGNMENT, LB_ERR_UNSUPPORTED, LB_ERR_CUDA.
  */
 lb_status lb_linear_int8(const int8_t *xq, int64_t ldx, const float *xs, int64_t M,
                          const int8_t *wq, int64_t ldw, const float *ws, int64_t in, int64_t out,
