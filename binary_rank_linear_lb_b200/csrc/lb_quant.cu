@@ -41,52 +41,139 @@ struct QuantArgs {
     float eps;
 };
 
-// A quotient this near a half-integer is computed again in 64 bits.  In fp32 v,
-// peak, 127 / peak and their product are each off by at most 2^-24 relative,
-// together by 4 * 2^-24 * 127 = 2^-15.01 for a quotient of at most 127.
-constexpr float kBorder = 1.0f / 16384.0f;
+// A quotient this near a half-integer is computed again in 64 bits.  v, peak and
+// 127 / peak are each off by at most 2^-24 relative in fp32 (the product is not
+// rounded before it is compared), together by 3 * 2^-24 * 127 = 2^-15.4 for a
+// quotient of at most 127.
+constexpr float kBorder = 1.0f / 32768.0f;
+// Adding it rounds |f| < 2^22 to a whole number, ties to even, and leaves that in
+// the low bits.
+constexpr float kRound = 12582912.0f;              // 1.5 * 2^23
 // Peaks and mean squares outside these are left to the 64-bit path (squares and
 // reciprocals inside them are far from fp32's ends).
 constexpr float kLow = 1e-30f, kHigh = 1e30f;
 
 constexpr int kMaxThreads = 1024;
+
+// Two fp32 at a time: sm_100 issues one instruction for both.
+struct F2 { unsigned long long u; };
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v.u));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return r;
+}
+// max(m, |v.x|, |v.y|); NaN if one is.
+__device__ __forceinline__ float max_abs(float m, F2 v) {
+    const float2 h = halves(v);
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(h.x), "f"(h.y));
+    return r;
+}
+
 // With this many rows or fewer a row takes four times the threads (8 elements each
 // instead of 32): its latency is what the call waits for.
 constexpr int64_t kFewRows = 148;
 
-// v[VE] = the VE elements at p, `n` of them inside the row (the rest 0).
-template <int DT, int VE, bool VEC>
-__device__ __forceinline__ void load_row(const typename Elem<DT>::T* p, int n, int stride, float (&v)[VE]) {
-    using X = Elem<DT>;
-    if constexpr (VEC) {
-        if (n >= VE) {
-            static_assert(VE * sizeof(typename X::T) == 16, "one 16-byte piece");
-            const uint4 u = *reinterpret_cast<const uint4*>(p);
-            const typename X::T* e = reinterpret_cast<const typename X::T*>(&u);
+// The VE elements of a 16-byte piece as pairs, and back.
+template <int DT> struct Piece;
+template <> struct Piece<LB_F32> {
+    static constexpr int VE = 4;
+    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[2]) {
+        v[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+        v[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 (&v)[2]) {
+        const float2 a = halves(v[0]), b = halves(v[1]);
+        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    }
+};
+template <> struct Piece<LB_BF16> {
+    static constexpr int VE = 8;
+    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[4]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < VE; ++i) v[i] = X::get(e[i]);
-            return;
+        for (int i = 0; i < 4; ++i) v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 (&v)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 h = halves(v[i]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(h.x, h.y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Piece<LB_F16> {
+    static constexpr int VE = 8;
+    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[4]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            v[i] = f2(f.x, f.y);
         }
     }
+    static __device__ __forceinline__ uint4 pack(const F2 (&v)[4]) {
+        uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) v[i] = i * (VEC ? 1 : stride) < n ? X::get(p[VEC ? i : i * stride]) : 0.0f;
-}
-template <int DT, int VE, bool VEC>
-__device__ __forceinline__ void store_row(typename Elem<DT>::T* p, int n, int stride, const float (&v)[VE]) {
-    using X = Elem<DT>;
-    if constexpr (VEC) {
-        if (n >= VE) {
-            uint4 u;
-            typename X::T* e = reinterpret_cast<typename X::T*>(&u);
-#pragma unroll
-            for (int i = 0; i < VE; ++i) e[i] = X::put(v[i]);
-            *reinterpret_cast<uint4*>(p) = u;
-            return;
+        for (int i = 0; i < 4; ++i) {
+            const float2 h = halves(v[i]);
+            const __half2 b = __floats2half2_rn(h.x, h.y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
+};
+
+// The piece at p, n of its elements inside the row (the rest 0).  VEC: 16
+// consecutive bytes; otherwise (pointers or pitches that are not multiples of
+// 16) elements `apart` columns from each other.
+template <int DT, bool VEC>
+__device__ __forceinline__ uint4 load_piece(const typename Elem<DT>::T* p, int n, int apart) {
+    using T = typename Elem<DT>::T;
+    constexpr int VE = Piece<DT>::VE;
+    if (VEC && n >= VE) return *reinterpret_cast<const uint4*>(p);
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    T* e = reinterpret_cast<T*>(&u);
 #pragma unroll
     for (int i = 0; i < VE; ++i)
-        if (i * (VEC ? 1 : stride) < n) p[VEC ? i : i * stride] = X::put(v[i]);
+        if (i * (VEC ? 1 : apart) < n) e[i] = p[VEC ? i : i * apart];
+    return u;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_piece(typename Elem<DT>::T* p, int n, int apart, uint4 u) {
+    using T = typename Elem<DT>::T;
+    constexpr int VE = Piece<DT>::VE;
+    if (VEC && n >= VE) {
+        *reinterpret_cast<uint4*>(p) = u;
+        return;
+    }
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+        if (i * (VEC ? 1 : apart) < n) p[VEC ? i : i * apart] = e[i];
 }
 
 __device__ __forceinline__ float weight_at(const void* w, int wt, int i) {
@@ -95,39 +182,41 @@ __device__ __forceinline__ float weight_at(const void* w, int wt, int i) {
     if (wt == LB_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
     return static_cast<const float*>(w)[i];
 }
-// The VE weights from column i (VEC: consecutive and 16-byte aligned pieces).
+// The weights of the piece of VE columns from i, as pairs.
 template <int VE, bool VEC>
-__device__ __forceinline__ void load_weights(const void* w, int wt, int i, int n, int stride, bool wide,
-                                             float (&v)[VE]) {
-    if (VEC && wide && n >= VE) {
-        if (wt == LB_F32) {
+__device__ __forceinline__ void load_weights(const QuantArgs& a, int i, int n, int apart, F2 (&v)[VE / 2]) {
+    if (VEC && a.weight_wide && n >= VE) {
+        if (a.weight_type == LB_F32) {
 #pragma unroll
             for (int j = 0; j < VE; j += 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + i + j));
-                v[j] = f.x; v[j + 1] = f.y; v[j + 2] = f.z; v[j + 3] = f.w;
+                const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + i + j));
+                v[j / 2] = f2(f.x, f.y);
+                v[j / 2 + 1] = f2(f.z, f.w);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < VE; j += 4) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + i + j));
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.weight) + i + j));
                 const uint32_t h[2] = {u.x, u.y};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float2 f = wt == LB_F16
+                    const float2 f = a.weight_type == LB_F16
                                          ? __half22float2(*reinterpret_cast<const __half2*>(&h[k]))
                                          : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h[k]));
-                    v[j + 2 * k] = f.x;
-                    v[j + 2 * k + 1] = f.y;
+                    v[j / 2 + k] = f2(f.x, f.y);
                 }
             }
         }
         return;
     }
+    float e[VE];
 #pragma unroll
     for (int j = 0; j < VE; ++j) {
-        const int o = VEC ? j : j * stride;
-        v[j] = o < n ? weight_at(w, wt, i + o) : 0.0f;
+        const int o = VEC ? j : j * apart;
+        e[j] = o < n ? weight_at(a.weight, a.weight_type, i + o) : 0.0f;
     }
+#pragma unroll
+    for (int j = 0; j < VE; j += 2) v[j / 2] = f2(e[j], e[j + 1]);
 }
 
 // Folds over the threads of a row: a warp (red unused) or the block.
@@ -181,140 +270,155 @@ __device__ __noinline__ void quant_row_64(const QuantArgs& a, int64_t row, int f
                    : (int8_t)code_d((double)X::get(s[i]), (double)weight_at(a.weight, a.weight_type, i), peak);
 }
 
-// C pieces of VE elements per thread.  VEC: a piece is 16 consecutive bytes;
-// otherwise (pointers or pitches that are not multiples of 16) its elements are
-// the row's threads apart, so that a warp still reads consecutive ones.
-template <int DT, int C, bool VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+// The codes of a piece again, those near a border in 64 bits: from memory, one
+// by one (rare: a border is that near for one quotient in 16,000).
+template <int DT>
+__device__ __noinline__ void settle_codes(const QuantArgs& a, int64_t row, int i, int apart, float inv,
+                                          double peak) {
     using X = Elem<DT>;
-    using T = typename X::T;
-    constexpr int VE = 16 / (int)sizeof(T);
+    const typename X::T* s = a.residual ? static_cast<const typename X::T*>(a.sum) + row * a.lds
+                                        : static_cast<const typename X::T*>(a.x) + row * a.ldx;
+#pragma unroll 1
+    for (int e = 0; e < Piece<DT>::VE; ++e, i += apart) {
+        if (i >= a.cols) return;
+        const float sv = X::get(s[i]), w = weight_at(a.weight, a.weight_type, i);
+        const float f = sv * w * inv;
+        // (f is rounded here, so the check is a little wider: 127 * 2^-24 < 2^-16)
+        if (fabsf(f - rintf(f)) >= 0.5f - 1.5f * kBorder)
+            a.q[row * a.ldq + i] = (int8_t)code_d((double)sv, (double)w, peak);
+    }
+}
+
+// C pieces of VE elements per thread; a warp per row (8 to a block) or a block
+// per row.  The work is as much in the instructions as in the bytes (a 16-bit
+// element comes and goes with 3 to 7 bytes), so everything runs on pairs and the
+// codes take two pair instructions: v * 127 / peak + kRound holds the code in its
+// low byte, and what it left over says how near the border was.
+template <int DT, int C, bool VEC, bool WARP, int THREADS>
+__global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+    using T = typename Elem<DT>::T;
+    constexpr int VE = Piece<DT>::VE, P = VE / 2;
     __shared__ double red[WARP ? 1 : 32];
     const int tr = WARP ? 32 : (int)blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
     if (WARP && row >= a.rows) return;
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.ldr : nullptr;
-    T* sum = a.residual ? static_cast<T*>(a.sum) + row * a.lds : nullptr;
-    const int estep = VEC ? 1 : tr;                // columns between a piece's elements
+    const int apart = VEC ? 1 : tr;                // columns between a piece's elements
     auto at = [&](int c) { return VEC ? (c * tr + t) * VE : c * tr * VE + t; };   // a piece's first column
 
-    // s, its squares, v = s w and the largest |v| (as bits: a NaN beats infinity)
-    float v[C][VE];
-    float ss = 0.0f;
-    uint32_t top = 0;
+    uint4 raw[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int i = at(c), n = a.cols - i;
-        if (n > 0) load_row<DT, VE, VEC>(x + i, n, estep, v[c]);
-        else
+    for (int c = 0; c < C; ++c) raw[c] = load_piece<DT, VEC>(x + at(c), a.cols - at(c), apart);
+    if (a.residual) {
+        const T* r = static_cast<const T*>(a.residual) + row * a.ldr;
+        T* sum = static_cast<T*>(a.sum) + row * a.lds;
+        uint4 more[C];
 #pragma unroll
-            for (int e = 0; e < VE; ++e) v[c][e] = 0.0f;
-    }
-    if (r) {
+        for (int c = 0; c < C; ++c) more[c] = load_piece<DT, VEC>(r + at(c), a.cols - at(c), apart);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int i = at(c), n = a.cols - i;
-            if (n <= 0) continue;
-            float rv[VE];
-            load_row<DT, VE, VEC>(r + i, n, estep, rv);
+            F2 xv[P], rv[P];
+            Piece<DT>::unpack(raw[c], xv);
+            Piece<DT>::unpack(more[c], rv);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) v[c][e] = X::get(X::put(v[c][e] + rv[e]));
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int i = at(c), n = a.cols - i;
-            if (n > 0) store_row<DT, VE, VEC>(sum + i, n, estep, v[c]);
+            for (int i = 0; i < P; ++i) xv[i] = add2(xv[i], rv[i]);
+            raw[c] = Piece<DT>::pack(xv);
+            store_piece<DT, VEC>(sum + at(c), a.cols - at(c), apart, raw[c]);
         }
     }
+    // v = s w, the sum of s^2 and the largest |v|
+    F2 v[C][P], sq = f2(0.0f, 0.0f);
+    float top = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int i = at(c), n = a.cols - i;
+        Piece<DT>::unpack(raw[c], v[c]);
         if (a.norm)
 #pragma unroll
-            for (int e = 0; e < VE; ++e) ss = fmaf(v[c][e], v[c][e], ss);
-        if (a.weight && n > 0) {
-            float w[VE];
-            load_weights<VE, VEC>(a.weight, a.weight_type, i, n, estep, a.weight_wide, w);
+            for (int i = 0; i < P; ++i) sq = fma2(v[c][i], v[c][i], sq);
+        if (a.weight) {
+            F2 w[P];
+            load_weights<VE, VEC>(a, at(c), a.cols - at(c), apart, w);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) v[c][e] *= w[e];
+            for (int i = 0; i < P; ++i) v[c][i] = mul2(v[c][i], w[i]);
         }
 #pragma unroll
-        for (int e = 0; e < VE; ++e) top = max(top, __float_as_uint(v[c][e]) & 0x7fffffffu);
+        for (int i = 0; i < P; ++i) top = max_abs(top, v[c][i]);
     }
-    // (the folds' scratch: one 8-byte word per warp)
-    struct Pair { float ss; uint32_t top; };
-    top = __reduce_max_sync(0xffffffffu, top);
+    float ss = halves(sq).x + halves(sq).y;
+    // non-negative floats order like their bits, and a NaN comes last
+    uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if constexpr (!WARP) {
-        Pair* pr = reinterpret_cast<Pair*>(red);
+        uint2* part = reinterpret_cast<uint2*>(red);
         const int nw = tr >> 5, lane = t & 31;
-        if (lane == 0) pr[t >> 5] = Pair{ss, top};
+        if (lane == 0) part[t >> 5] = make_uint2(__float_as_uint(ss), bits);
         __syncthreads();
-        const Pair mine = lane < nw ? pr[lane] : Pair{0.0f, 0u};
-        ss = mine.ss;
-        top = __reduce_max_sync(0xffffffffu, mine.top);
+        const uint2 mine = lane < nw ? part[lane] : make_uint2(0u, 0u);
+        ss = __uint_as_float(mine.x);
+        bits = __reduce_max_sync(0xffffffffu, mine.y);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    const float peak = __uint_as_float(top);
+    const float peak = __uint_as_float(bits);
     const float ms = ss / (float)a.cols;
     if (!(peak >= kLow && peak <= kHigh) || (a.norm && !(ms >= kLow && ms <= kHigh))) {
         quant_row_64<DT, WARP>(a, row, t, tr, red);
         return;
     }
     // the exact peak: of the products that round to it, the largest in 64 bits
-    const T* src = r ? sum : x;
     double exact = (double)peak;
     if (a.inexact) {
+        const T* s = a.residual ? static_cast<const T*>(a.sum) + row * a.lds : x;
         exact = 0.0;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int e = 0; e < VE; ++e)
-                if (fabsf(v[c][e]) == peak) {
-                    const int i = at(c) + e * estep;
-                    exact = fmax(exact, fabs((double)X::get(src[i]) * (double)weight_at(a.weight, a.weight_type, i)));
-                }
+            for (int i = 0; i < P; ++i) {
+                const float2 h = halves(v[c][i]);
+                if (fmaxf(fabsf(h.x), fabsf(h.y)) == peak)
+#pragma unroll 1
+                    for (int e = 0; e < 2; ++e) {
+                        const int o = at(c) + (2 * i + e) * apart;
+                        if (o < a.cols)
+                            exact = fmax(exact, fabs((double)Elem<DT>::get(s[o]) *
+                                                     (double)weight_at(a.weight, a.weight_type, o)));
+                    }
+            }
         exact = row_fold<WARP>(exact, 0.0, red, max_d);
     }
     if (t == 0) a.scale[row] = a.norm ? peak / (127.0f * sqrtf(ms + a.eps)) : peak / 127.0f;
     const float inv = 127.0f / peak;
+    const F2 inv2 = f2(inv, inv), round2 = f2(kRound, kRound), back2 = f2(-kRound, -kRound);
+    const F2 minus2 = f2(-1.0f, -1.0f);
     int8_t* q = a.q + row * a.ldq;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = at(c), n = a.cols - i;
-        int8_t code[VE];
-        bool near = false;
+        uint32_t code[VE];
+        float rest = 0.0f;                         // the largest distance from a code
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            const float f = v[c][e] * inv, k = rintf(f);
-            near |= fabsf(f - k) >= 0.5f - kBorder;
-            code[e] = (int8_t)__float2int_rn(k);
+        for (int j = 0; j < P; ++j) {
+            const F2 k = fma2(v[c][j], inv2, round2);
+            const float2 h = halves(k);
+            code[2 * j] = __float_as_uint(h.x);
+            code[2 * j + 1] = __float_as_uint(h.y);
+            const F2 whole = mul2(add2(k, back2), minus2);
+            rest = max_abs(rest, fma2(v[c][j], inv2, whole));
         }
-        if (near)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float f = v[c][e] * inv;
-                const int o = i + e * estep;
-                if (fabsf(f - rintf(f)) >= 0.5f - kBorder && o < a.cols)
-                    code[e] = (int8_t)code_d((double)X::get(src[o]), (double)weight_at(a.weight, a.weight_type, o), exact);
-            }
-        if (n <= 0) continue;
         if (VEC && n >= VE) {
             uint32_t w[VE / 4];
 #pragma unroll
             for (int e = 0; e < VE; e += 4)
-                w[e / 4] = (uint32_t)(uint8_t)code[e] | (uint32_t)(uint8_t)code[e + 1] << 8 |
-                           (uint32_t)(uint8_t)code[e + 2] << 16 | (uint32_t)(uint8_t)code[e + 3] << 24;
+                w[e / 4] = prmt(prmt(code[e], code[e + 1], 0x0040u), prmt(code[e + 2], code[e + 3], 0x0040u), 0x5410u);
             if constexpr (VE == 8) *reinterpret_cast<uint2*>(q + i) = make_uint2(w[0], w[1]);
             else *reinterpret_cast<uint32_t*>(q + i) = w[0];
         } else {
 #pragma unroll
             for (int e = 0; e < VE; ++e)
-                if (e * estep < n) q[i + e * estep] = code[e];
+                if (e * apart < n) q[i + e * apart] = (int8_t)code[e];
         }
+        if (rest >= 0.5f - kBorder) settle_codes<DT>(a, row, i, apart, inv, exact);
     }
 }
 
@@ -334,25 +438,27 @@ __global__ void __launch_bounds__(256) quant_wide_kernel(const __grid_constant__
     quant_row_64<DT, false>(a, row, threadIdx.x, 256, red);
 }
 
-template <int DT, int C, bool VEC>
-void launch_block(const QuantArgs& a, int per_piece, cudaStream_t s) {
-    const int threads = ((a.cols + C * per_piece - 1) / (C * per_piece) + 31) / 32 * 32;
-    quant_rows_kernel<DT, C, VEC, false><<<(unsigned)a.rows, threads, 0, s>>>(a);
+template <int DT, int C, bool VEC, int THREADS>
+void launch_block(const QuantArgs& a, cudaStream_t s) {
+    constexpr int per_thread = C * Piece<DT>::VE;
+    const int threads = ((a.cols + per_thread - 1) / per_thread + 31) / 32 * 32;
+    quant_rows_kernel<DT, C, VEC, false, THREADS><<<(unsigned)a.rows, threads, 0, s>>>(a);
 }
 
 template <int DT, bool VEC>
 void launch_rows(const QuantArgs& a, cudaStream_t s) {
-    constexpr int VE = 16 / (int)sizeof(typename Elem<DT>::T);
-    constexpr int kFull = 32 / VE;                 // pieces of 32 elements
-    constexpr int kFew = 8 / VE;                   // pieces of 8 elements
+    constexpr int kFull = 32 / Piece<DT>::VE;      // pieces of 32 elements
+    constexpr int kFew = 8 / Piece<DT>::VE;        // pieces of 8 elements
     if (a.cols <= 32 * 32) {
         const unsigned blocks = (unsigned)((a.rows + 7) / 8);
-        if (a.cols <= 32 * 8) quant_rows_kernel<DT, kFew, VEC, true><<<blocks, 256, 0, s>>>(a);
-        else quant_rows_kernel<DT, kFull, VEC, true><<<blocks, 256, 0, s>>>(a);
+        if (a.cols <= 32 * 8) quant_rows_kernel<DT, kFew, VEC, true, 256><<<blocks, 256, 0, s>>>(a);
+        else quant_rows_kernel<DT, kFull, VEC, true, 256><<<blocks, 256, 0, s>>>(a);
     } else if (a.cols <= kMaxThreads * 8 && a.rows <= kFewRows) {
-        launch_block<DT, kFew, VEC>(a, VE, s);
+        launch_block<DT, kFew, VEC, kMaxThreads>(a, s);
+    } else if (a.cols <= 256 * 32) {
+        launch_block<DT, kFull, VEC, 256>(a, s);
     } else if (a.cols <= kMaxThreads * 32) {
-        launch_block<DT, kFull, VEC>(a, VE, s);
+        launch_block<DT, kFull, VEC, kMaxThreads>(a, s);
     } else {
         quant_wide_kernel<DT><<<(unsigned)a.rows, 256, 0, s>>>(a);
     }
