@@ -294,11 +294,12 @@ __device__ __noinline__ void settle_codes(const QuantArgs& a, int64_t row, int i
 // element comes and goes with 3 to 7 bytes), so everything runs on pairs and the
 // codes take two pair instructions: v * 127 / peak + kRound holds the code in its
 // low byte, and what it left over says how near the border was.
-template <int DT, int C, bool VEC, bool WARP, int THREADS>
+template <int DT, int C, bool VEC, bool WARP, int THREADS, bool NORM>
 __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int VE = Piece<DT>::VE, P = VE / 2;
     __shared__ double red[WARP ? 1 : 32];
+    __shared__ unsigned long long exact_bits[WARP ? 8 : 1];
     const int tr = WARP ? 32 : (int)blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
     if (WARP && row >= a.rows) return;
@@ -309,7 +310,14 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
     uint4 raw[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) raw[c] = load_piece<DT, VEC>(x + at(c), a.cols - at(c), apart);
-    if (a.residual) {
+    // with 8 elements a thread (few rows) the weights are requested with the row
+    constexpr bool kEarly = NORM && C * VE == 8;
+    F2 we[kEarly ? C : 1][P];
+    if constexpr (kEarly)
+        if (a.weight)
+#pragma unroll
+            for (int c = 0; c < C; ++c) load_weights<VE, VEC>(a, at(c), a.cols - at(c), apart, we[c]);
+    if (NORM && a.residual) {
         const T* r = static_cast<const T*>(a.residual) + row * a.ldr;
         T* sum = static_cast<T*>(a.sum) + row * a.lds;
         uint4 more[C];
@@ -326,26 +334,32 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
             store_piece<DT, VEC>(sum + at(c), a.cols - at(c), apart, raw[c]);
         }
     }
-    // v = s w, the sum of s^2 and the largest |v|
-    F2 v[C][P], sq = f2(0.0f, 0.0f);
+    // v = s w, the sum of s^2 and the largest |v|.  (Without a norm v is the row
+    // itself and is unpacked again for the codes, which frees registers.)
+    F2 v[NORM ? C : 1][P], sq = f2(0.0f, 0.0f);
     float top = 0.0f;
+    const int slot = WARP ? threadIdx.x >> 5 : 0;
+    if (t == 0) exact_bits[slot] = 0;              // (ordered before its use by the barriers below)
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        Piece<DT>::unpack(raw[c], v[c]);
-        if (a.norm)
+        F2 (&vc)[P] = v[NORM ? c : 0];
+        Piece<DT>::unpack(raw[c], vc);
+        if (NORM) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) sq = fma2(v[c][i], v[c][i], sq);
-        if (a.weight) {
-            F2 w[P];
-            load_weights<VE, VEC>(a, at(c), a.cols - at(c), apart, w);
+            for (int i = 0; i < P; ++i) sq = fma2(vc[i], vc[i], sq);
+            if (a.weight) {
+                F2 w[P];
+                if constexpr (!kEarly) load_weights<VE, VEC>(a, at(c), a.cols - at(c), apart, w);
 #pragma unroll
-            for (int i = 0; i < P; ++i) v[c][i] = mul2(v[c][i], w[i]);
+                for (int i = 0; i < P; ++i) vc[i] = mul2(vc[i], kEarly ? we[c][i] : w[i]);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < P; ++i) top = max_abs(top, v[c][i]);
+        for (int i = 0; i < P; ++i) top = max_abs(top, vc[i]);
     }
     float ss = halves(sq).x + halves(sq).y;
     // non-negative floats order like their bits, and a NaN comes last
+    __syncwarp();
     uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -362,49 +376,53 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
     }
     const float peak = __uint_as_float(bits);
     const float ms = ss / (float)a.cols;
-    if (!(peak >= kLow && peak <= kHigh) || (a.norm && !(ms >= kLow && ms <= kHigh))) {
+    if (!(peak >= kLow && peak <= kHigh) || (NORM && !(ms >= kLow && ms <= kHigh))) {
         quant_row_64<DT, WARP>(a, row, t, tr, red);
         return;
     }
-    // the exact peak: of the products that round to it, the largest in 64 bits
-    double exact = (double)peak;
-    if (a.inexact) {
+    // The exact peak: of the products that round to it, the largest in 64 bits.  It
+    // is only needed where a code is near a border, so the threads that hold those
+    // products leave it in shared memory and it is read after the codes.
+    if (NORM && a.inexact) {
         const T* s = a.residual ? static_cast<const T*>(a.sum) + row * a.lds : x;
-        exact = 0.0;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const float2 h = halves(v[c][i]);
+                const float2 h = halves(v[NORM ? c : 0][i]);
                 if (fmaxf(fabsf(h.x), fabsf(h.y)) == peak)
 #pragma unroll 1
                     for (int e = 0; e < 2; ++e) {
                         const int o = at(c) + (2 * i + e) * apart;
-                        if (o < a.cols)
-                            exact = fmax(exact, fabs((double)Elem<DT>::get(s[o]) *
-                                                     (double)weight_at(a.weight, a.weight_type, o)));
+                        if (o < a.cols)          // (non-negative doubles order like their bits)
+                            atomicMax(&exact_bits[slot],
+                                      (unsigned long long)__double_as_longlong(fabs(
+                                          (double)Elem<DT>::get(s[o]) *
+                                          (double)weight_at(a.weight, a.weight_type, o))));
                     }
             }
-        exact = row_fold<WARP>(exact, 0.0, red, max_d);
     }
-    if (t == 0) a.scale[row] = a.norm ? peak / (127.0f * sqrtf(ms + a.eps)) : peak / 127.0f;
+    if (t == 0) a.scale[row] = NORM ? peak / (127.0f * sqrtf(ms + a.eps)) : peak / 127.0f;
     const float inv = 127.0f / peak;
     const F2 inv2 = f2(inv, inv), round2 = f2(kRound, kRound), back2 = f2(-kRound, -kRound);
     const F2 minus2 = f2(-1.0f, -1.0f);
     int8_t* q = a.q + row * a.ldq;
+    uint32_t near = 0;                             // pieces with a code near a border
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = at(c), n = a.cols - i;
+        F2 (&vc)[P] = v[NORM ? c : 0];
+        if (!NORM) Piece<DT>::unpack(raw[c], vc);
         uint32_t code[VE];
         float rest = 0.0f;                         // the largest distance from a code
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            const F2 k = fma2(v[c][j], inv2, round2);
+            const F2 k = fma2(vc[j], inv2, round2);
             const float2 h = halves(k);
             code[2 * j] = __float_as_uint(h.x);
             code[2 * j + 1] = __float_as_uint(h.y);
             const F2 whole = mul2(add2(k, back2), minus2);
-            rest = max_abs(rest, fma2(v[c][j], inv2, whole));
+            rest = max_abs(rest, fma2(vc[j], inv2, whole));
         }
         if (VEC && n >= VE) {
             uint32_t w[VE / 4];
@@ -418,7 +436,18 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
             for (int e = 0; e < VE; ++e)
                 if (e * apart < n) q[i + e * apart] = (int8_t)code[e];
         }
-        if (rest >= 0.5f - kBorder) settle_codes<DT>(a, row, i, apart, inv, exact);
+        near |= rest >= 0.5f - kBorder ? 1u << c : 0u;
+    }
+    double exact = (double)peak;
+    if (NORM && a.inexact) {
+        if constexpr (WARP) __syncwarp();
+        else __syncthreads();
+        exact = __longlong_as_double((long long)exact_bits[slot]);
+    }
+    while (near) {
+        const int c = __ffs(near) - 1;
+        near &= near - 1;
+        settle_codes<DT>(a, row, at(c), apart, inv, exact);
     }
 }
 
@@ -438,27 +467,27 @@ __global__ void __launch_bounds__(256) quant_wide_kernel(const __grid_constant__
     quant_row_64<DT, false>(a, row, threadIdx.x, 256, red);
 }
 
-template <int DT, int C, bool VEC, int THREADS>
+template <int DT, int C, bool VEC, int THREADS, bool NORM>
 void launch_block(const QuantArgs& a, cudaStream_t s) {
     constexpr int per_thread = C * Piece<DT>::VE;
     const int threads = ((a.cols + per_thread - 1) / per_thread + 31) / 32 * 32;
-    quant_rows_kernel<DT, C, VEC, false, THREADS><<<(unsigned)a.rows, threads, 0, s>>>(a);
+    quant_rows_kernel<DT, C, VEC, false, THREADS, NORM><<<(unsigned)a.rows, threads, 0, s>>>(a);
 }
 
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool NORM>
 void launch_rows(const QuantArgs& a, cudaStream_t s) {
     constexpr int kFull = 32 / Piece<DT>::VE;      // pieces of 32 elements
     constexpr int kFew = 8 / Piece<DT>::VE;        // pieces of 8 elements
     if (a.cols <= 32 * 32) {
         const unsigned blocks = (unsigned)((a.rows + 7) / 8);
-        if (a.cols <= 32 * 8) quant_rows_kernel<DT, kFew, VEC, true, 256><<<blocks, 256, 0, s>>>(a);
-        else quant_rows_kernel<DT, kFull, VEC, true, 256><<<blocks, 256, 0, s>>>(a);
+        if (a.cols <= 32 * 8) quant_rows_kernel<DT, kFew, VEC, true, 256, NORM><<<blocks, 256, 0, s>>>(a);
+        else quant_rows_kernel<DT, kFull, VEC, true, 256, NORM><<<blocks, 256, 0, s>>>(a);
     } else if (a.cols <= kMaxThreads * 8 && a.rows <= kFewRows) {
-        launch_block<DT, kFew, VEC, kMaxThreads>(a, s);
+        launch_block<DT, kFew, VEC, kMaxThreads, NORM>(a, s);
     } else if (a.cols <= 256 * 32) {
-        launch_block<DT, kFull, VEC, 256>(a, s);
+        launch_block<DT, kFull, VEC, 256, NORM>(a, s);
     } else if (a.cols <= kMaxThreads * 32) {
-        launch_block<DT, kFull, VEC, kMaxThreads>(a, s);
+        launch_block<DT, kFull, VEC, kMaxThreads, NORM>(a, s);
     } else {
         quant_wide_kernel<DT><<<(unsigned)a.rows, 256, 0, s>>>(a);
     }
@@ -476,8 +505,8 @@ lb_status quant_call(QuantArgs a, int dt, cudaStream_t s) {
     // products that fp32 holds exactly: two 16-bit factors, or no weight
     a.inexact = a.weight && (dt == LB_F32 || a.weight_type == LB_F32);
     with_dtype(dt, [&](auto d) {
-        if (vec) launch_rows<d.value, true>(a, s);
-        else launch_rows<d.value, false>(a, s);
+        if (a.norm) vec ? launch_rows<d.value, true, true>(a, s) : launch_rows<d.value, false, true>(a, s);
+        else vec ? launch_rows<d.value, true, false>(a, s) : launch_rows<d.value, false, false>(a, s);
     });
     return cudaGetLastError() == cudaSuccess ? LB_OK : LB_ERR_CUDA;
 }
