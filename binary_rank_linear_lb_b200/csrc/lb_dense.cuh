@@ -1,5 +1,5 @@
 // Shared by the dense-path operators (lb_quant.cu, lb_int8.cu, lb_logprobs.cu):
-// element types, argument helpers.
+// element types, pair arithmetic, argument helpers.
 #pragma once
 
 #include "lb_internal.cuh"
@@ -23,6 +23,87 @@ template <> struct Elem<LB_F32> {
     using T = float;
     static __device__ __forceinline__ float get(T v) { return v; }
     static __device__ __forceinline__ T put(float v) { return v; }
+};
+
+// Two fp32 at a time: sm_100 issues one instruction for both.
+struct F2 { unsigned long long u; };
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v.u));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return r;
+}
+
+// The VE elements of a 16-byte piece as pairs, and back.
+template <int DT> struct Piece;
+template <> struct Piece<LB_F32> {
+    static constexpr int VE = 4;
+    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[2]) {
+        v[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+        v[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 (&v)[2]) {
+        const float2 a = halves(v[0]), b = halves(v[1]);
+        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    }
+};
+template <> struct Piece<LB_BF16> {
+    static constexpr int VE = 8;
+    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[4]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 (&v)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 h = halves(v[i]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(h.x, h.y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Piece<LB_F16> {
+    static constexpr int VE = 8;
+    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[4]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            v[i] = f2(f.x, f.y);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 (&v)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 h = halves(v[i]);
+            const __half2 b = __floats2half2_rn(h.x, h.y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
 
 inline bool dtype_ok(int t) { return t == LB_F16 || t == LB_BF16 || t == LB_F32; }

@@ -3,6 +3,25 @@
 //   entropy = -sum p_i log p_i = log S - sum e^(x - m) (x - m) / S,
 // the log probabilities of the given tokens and of the `top` largest logits.
 // Both terms of the entropy are >= 0, so nothing cancels.
+//
+// One pass.  Every thread keeps the running maximum, S and the entropy's sum of
+// its 16-byte pieces (rescaled when the maximum grows, which after the first
+// batches is rare), in powers of two: t = (x - m) log2 e, S = sum 2^t,
+// A = sum 2^t t.  The threads' triples are folded at the end.  What bounds it:
+// HBM for fp32, the exponentials (16 a clock and SM) and the instructions around
+// them (about 5 an element) close behind for 16-bit logits.
+//
+// The alternatives need no second pass either: the threads' maxima bound them.
+// If T is the top-th largest of the maxima, at least `top` logits are >= T, so
+// the alternatives are among the logits >= T, and only threads whose maximum is
+// >= T hold any: those few read their pieces again (from L2).  T is found by
+// bisection over the maxima (any bound with `top` maxima above it will do), the
+// candidates are ranked by counting.  Where many logits equal T (a mask that leaves
+// few) only the first of those are taken; rows where too many lie above it, or
+// with a NaN, take `top` rounds of a maximum instead.
+//
+// With few rows a row is split over a cluster of CTAs; the first one folds the
+// others' results through distributed shared memory.
 #include <cmath>
 
 #include "lb_dense.cuh"
@@ -11,7 +30,14 @@ namespace lb {
 namespace {
 
 constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;
+constexpr int kCandidates = 1024;            // logits >= T kept at most
+constexpr int kLpCluster = 8;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// t below this is as good as -inf (2^t is 0), and unlike it can be multiplied by 0.
+constexpr float kTiny = -200.0f;
 
 struct LogprobArgs {
     const void* x;
@@ -25,82 +51,395 @@ struct LogprobArgs {
 };
 
 // Order of the alternatives as an unsigned key: larger logit first, NaN before
-// everything, -0 equal to +0.
+// everything, -0 equal to +0.  Key 0 is below every logit.
 __device__ __forceinline__ uint32_t order_key(float v) {
     if (v != v) return 0xffffffffu;
     const uint32_t u = __float_as_uint(v + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return k == 0xffffffffu ? NAN : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+// Key and index as one number: larger is earlier (equal keys by rising index).
+__device__ __forceinline__ unsigned long long entry_of(uint32_t key, int i) {
+    return (unsigned long long)key << 32 | (0xffffffffu - (uint32_t)i);
+}
+__device__ __forceinline__ int entry_index(unsigned long long e) { return (int)(0xffffffffu - (uint32_t)e); }
 
-// One block per row; `top` rounds, each the largest (key, lowest index) below
-// the one before it.
-template <int DT>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobArgs a) {
-    using X = Elem<DT>;
-    __shared__ float fred[3][kLpThreads / 32];
-    __shared__ unsigned long long kred[kLpThreads / 32];
-    const int64_t row = blockIdx.x;
-    const typename X::T* x = static_cast<const typename X::T*>(a.x) + row * a.ld;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float m = -INFINITY;
+__device__ __forceinline__ float exp2_fast(float t) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+    return r;
+}
+__device__ __forceinline__ float max3_nan(float a, F2 v) {
+    const float2 h = halves(v);
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(h.x), "f"(h.y));
+    return r;
+}
+
+// Running maximum and sums of a thread.
+struct Stat {
+    float m = -INFINITY, shift = 0.0f;             // shift: m, or 0 while m = -inf
+    F2 S = {0ull}, A = {0ull};
     bool nan = false;
-    for (int i = threadIdx.x; i < a.vocab; i += kLpThreads) {
-        const float v = X::get(x[i]);
-        nan |= v != v;
-        m = fmaxf(m, v);
-    }
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) fred[0][warp] = m;
-    nan = __syncthreads_or(nan) != 0;
-    for (int w = 0; w < kLpThreads / 32; ++w) m = fmaxf(m, fred[0][w]);
-    const bool empty = m == -INFINITY && !nan;
-    float S = 0.0f, A = 0.0f;
-    if (!empty)
-        for (int i = threadIdx.x; i < a.vocab; i += kLpThreads) {
-            const float d = X::get(x[i]) - m, e = expf(d);
-            S += e;
-            if (e > 0.0f) A += e * d;
+
+    template <int P>
+    __device__ __forceinline__ void take(const F2 (&x)[P]) {
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < P; ++i) top = max3_nan(top, x[i]);
+        if (!(top <= m)) {
+            if (top != top) {
+                nan = true;
+            } else {
+                if (m > -INFINITY) {
+                    const float dt = fmaxf((m - top) * kLog2e, kTiny), c = exp2_fast(dt);
+                    A = mul2(f2(c, c), fma2(S, f2(dt, dt), A));
+                    S = mul2(f2(c, c), S);
+                }
+                m = shift = top;
+            }
         }
+        const F2 back = f2(-shift, -shift), l2e = f2(kLog2e, kLog2e);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float2 t = halves(mul2(add2(x[i], back), l2e));
+            t.x = fmaxf(t.x, kTiny);
+            t.y = fmaxf(t.y, kTiny);
+            const F2 e = f2(exp2_fast(t.x), exp2_fast(t.y));
+            S = add2(S, e);
+            A = fma2(e, f2(t.x, t.y), A);
+        }
+    }
+};
+
+// What a CTA knows of its part of a row.
+struct LpPart {
+    float m, S, A;
+    int nan;
+    unsigned long long list[kMaxTop];              // its alternatives, in order (0: none left)
+};
+
+__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
+    uint32_t p;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
+    return p;
+}
+__device__ __forceinline__ uint32_t ld_peer32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long ld_peer64(uint32_t addr) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A CTA per row, or `parts` CTAs (a cluster).  A row is read as the 16-byte
+// pieces of memory that it touches; the first and the last may lie partly
+// outside it and are read element by element.
+template <int DT, bool SPLIT>
+__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_constant__ LogprobArgs a, int parts) {
+    using X = Elem<DT>;
+    using T = typename X::T;
+    constexpr int VE = Piece<DT>::VE;
+    constexpr int kBatch = 16 / VE;                // pieces of a batch: 16 logits
+    __shared__ float fred[2][kLpWarps];
+    __shared__ uint32_t kmax[kLpWarps], kmin[kLpWarps];
+    __shared__ int n_cand;
+    __shared__ unsigned long long cand[kCandidates];
+    __shared__ LpPart part;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = SPLIT ? (int)(blockIdx.x % parts) : 0;
+    const int64_t row = SPLIT ? blockIdx.x / parts : blockIdx.x;
+    const T* x = static_cast<const T*>(a.x) + row * a.ld;
+    const int shift = (int)(reinterpret_cast<uintptr_t>(x) & 15) / (int)sizeof(T);
+    const int n_pieces = (shift + a.vocab + VE - 1) / VE;
+    const int p0 = SPLIT ? (int)((int64_t)n_pieces * rank / parts) : 0;
+    const int p1 = SPLIT ? (int)((int64_t)n_pieces * (rank + 1) / parts) : n_pieces;
+
+    // the given token's logit is requested first
+    int64_t tok = -1;
+    float tok_x = 0.0f;
+    if (threadIdx.x == 0 && rank == 0 && a.tokens) {
+        tok = a.tokens[row];
+        if (tok >= 0 && tok < a.vocab) tok_x = X::get(x[tok]);
+    }
+    if (threadIdx.x == 0) n_cand = 0;
+
+    auto load = [&](int j) {
+        const int i = j * VE - shift;
+        if (i >= 0 && i + VE <= a.vocab && j < p1) return __ldg(reinterpret_cast<const uint4*>(x + i));
+        const float none = -INFINITY;
+        uint4 u;
+        T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+        for (int k = 0; k < VE; ++k) e[k] = j < p1 && i + k >= 0 && i + k < a.vocab ? x[i + k] : X::put(none);
+        return u;
+    };
+
+    Stat st;
+    for (int j = p0 + (int)threadIdx.x; j < p1; j += kBatch * kLpThreads) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) raw[b] = load(j + b * kLpThreads);
+        F2 v[8];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            F2 (&vb)[VE / 2] = *reinterpret_cast<F2 (*)[VE / 2]>(&v[b * VE / 2]);
+            Piece<DT>::unpack(raw[b], vb);
+        }
+        st.take(v);
+    }
+
+    // fold: the row's maximum (as a key), then the sums relative to it
+    const bool some = p0 + (int)threadIdx.x < p1;            // this thread holds logits
+    const uint32_t key = some ? order_key(st.m) : 0u;
+    {
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, key);
+        const uint32_t lo = __reduce_min_sync(0xffffffffu, some ? key : 0xffffffffu);
+        if (lane == 0) { kmax[warp] = hi; kmin[warp] = lo; }
+    }
+    const bool nan = __syncthreads_or(st.nan) != 0;
+    uint32_t hi = 0, lo = 0xffffffffu;
+#pragma unroll
+    for (int w = 0; w < kLpWarps; ++w) { hi = max(hi, kmax[w]); lo = min(lo, kmin[w]); }
+    const float M = hi ? key_value(hi) : -INFINITY;
+    float S = halves(st.S).x + halves(st.S).y, A = halves(st.A).x + halves(st.A).y;
+    if (M > -INFINITY) {
+        const float dt = fmaxf((st.m - M) * kLog2e, kTiny), c = exp2_fast(dt);
+        A = c * fmaf(S, dt, A);
+        S *= c;
+    }
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         S += __shfl_xor_sync(0xffffffffu, S, o);
         A += __shfl_xor_sync(0xffffffffu, A, o);
     }
-    if (lane == 0) { fred[1][warp] = S; fred[2][warp] = A; }
+    if (lane == 0) { fred[0][warp] = S; fred[1][warp] = A; }
+
+    if (a.top > 0) {
+        const int held = (n_pieces < p1 ? n_pieces : p1) - p0;             // pieces of this part
+        bool rounds = nan;
+        if (!rounds) {
+            // T: at least `top` of the threads' maxima are >= T (0: every logit is a candidate)
+            uint32_t T0 = 0;
+            if (held >= a.top && kLpThreads >= a.top) {
+                T0 = lo;
+                uint32_t end = hi;                                         // T0 <= T < end + 1
+                while (T0 < end) {
+                    const uint32_t mid = T0 + (end - T0 + 1) / 2;
+                    const int c = __syncthreads_count(some && key >= mid);
+                    if (c >= a.top) {
+                        T0 = mid;
+                        if (c <= a.top + a.top / 4 + 1) break;
+                    } else {
+                        end = mid - 1;
+                    }
+                }
+            }
+            // the logits >= from that the threads with a maximum >= from hold
+            auto gather = [&](uint32_t from) {
+                if (some && key >= from)
+                    for (int j = p0 + (int)threadIdx.x; j < p1; j += kBatch * kLpThreads) {
+                        uint4 raw[kBatch];
+#pragma unroll
+                        for (int b = 0; b < kBatch; ++b) raw[b] = load(j + b * kLpThreads);
+#pragma unroll
+                        for (int b = 0; b < kBatch; ++b) {
+                            const T* e = reinterpret_cast<const T*>(&raw[b]);
+                            const int i = (j + b * kLpThreads) * VE - shift;
+                            if (j + b * kLpThreads >= p1) break;
+#pragma unroll
+                            for (int k = 0; k < VE; ++k) {
+                                const uint32_t ek = order_key(X::get(e[k]));
+                                if (ek >= from && i + k >= 0 && i + k < a.vocab) {
+                                    const int at = atomicAdd(&n_cand, 1);
+                                    if (at < kCandidates) cand[at] = entry_of(ek, i + k);
+                                }
+                            }
+                        }
+                    }
+                __syncthreads();
+            };
+            gather(T0);
+            if (n_cand > kCandidates) {
+                // Many equal T (a mask that leaves few, a constant row): take those above
+                // it, and the first of the equal ones as a warp meets them in order.
+                __syncthreads();
+                if (threadIdx.x == 0) n_cand = 0;
+                __syncthreads();
+                gather(T0 + 1);
+                const int above = n_cand;
+                rounds = above > kCandidates - kMaxTop;
+                __syncthreads();
+                if (!rounds && warp == 0) {
+                    int found = above;
+                    for (int j = p0; j < p1 && found < a.top; j += 32) {
+                        const uint4 raw = load(j + lane);
+                        const T* e = reinterpret_cast<const T*>(&raw);
+                        const int i = (j + lane) * VE - shift;
+                        uint32_t equal = 0;
+#pragma unroll
+                        for (int k = 0; k < VE; ++k)
+                            if (j + lane < p1 && i + k >= 0 && i + k < a.vocab && order_key(X::get(e[k])) == T0)
+                                equal |= 1u << k;
+                        int upto = __popc(equal);
+#pragma unroll
+                        for (int o = 1; o < 32; o *= 2) {
+                            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                            if (lane >= o) upto += v;
+                        }
+                        int at = found + upto - __popc(equal);
+                        for (; equal && at < a.top; equal &= equal - 1) cand[at++] = entry_of(T0, i + __ffs(equal) - 1);
+                        found += __shfl_sync(0xffffffffu, upto, 31);
+                    }
+                    if (lane == 0) n_cand = max(above, min(found, a.top));
+                }
+                __syncthreads();
+            }
+        }
+        if (!rounds) {
+            const int n = n_cand;
+            for (int c = threadIdx.x; c < n; c += kLpThreads) {
+                const unsigned long long mine = cand[c];
+                int before = 0;
+                for (int o = 0; o < n; ++o) before += cand[o] > mine;
+                if (before < a.top) part.list[before] = mine;
+            }
+            if ((int)threadIdx.x >= n && (int)threadIdx.x < a.top) part.list[threadIdx.x] = 0;
+        } else {
+            // the largest entry below the one before it, `top` times
+            unsigned long long last = ~0ull;
+            for (int k = 0; k < a.top; ++k) {
+                unsigned long long best = 0;
+                for (int j = p0 + (int)threadIdx.x; j < p1; j += kLpThreads) {
+                    const uint4 raw = load(j);
+                    const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                    for (int q = 0; q < VE; ++q) {
+                        const int i = j * VE - shift + q;
+                        const unsigned long long c = entry_of(order_key(X::get(e[q])), i);
+                        if (i >= 0 && i < a.vocab && c < last && c > best) best = c;
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const unsigned long long c = __shfl_xor_sync(0xffffffffu, best, o);
+                    best = c > best ? c : best;
+                }
+                __syncthreads();                                            // cand is free again
+                if (lane == 0) cand[warp] = best;
+                __syncthreads();
+                for (int w = 0; w < kLpWarps; ++w) best = cand[w] > best ? cand[w] : best;
+                last = best;
+                if (threadIdx.x == 0) part.list[k] = best;
+            }
+        }
+    }
     __syncthreads();
-    S = A = 0.0f;
-    for (int w = 0; w < kLpThreads / 32; ++w) { S += fred[1][w]; A += fred[2][w]; }
-    const bool bad = nan || m == INFINITY;
-    const float logS = logf(S);
-    auto logprob = [&](float v) { return bad ? NAN : empty ? -INFINITY : (v - m) - logS; };
     if (threadIdx.x == 0) {
-        if (a.entropy) a.entropy[row] = bad ? NAN : empty ? 0.0f : logS - A / S;
-        if (a.tokens) {
-            const int64_t t = a.tokens[row];
-            a.logprob[row] = t < 0 ? 0.0f : t >= a.vocab ? NAN : logprob(X::get(x[t]));
-        }
+        S = A = 0.0f;
+        for (int w = 0; w < kLpWarps; ++w) { S += fred[0][w]; A += fred[1][w]; }
+        part.m = M; part.S = S; part.A = A; part.nan = nan;
     }
-    unsigned long long last = ~0ull;
-    for (int k = 0; k < a.top; ++k) {
-        unsigned long long best = 0;
-        for (int i = threadIdx.x; i < a.vocab; i += kLpThreads) {
-            const unsigned long long c = (unsigned long long)order_key(X::get(x[i])) << 32 | (0xffffffffu - i);
-            if (c < last && c > best) best = c;
+    __syncthreads();
+
+    if constexpr (SPLIT) {
+        // the first CTA gathers the others' parts
+        cluster_sync();
+        if (rank == 0) {
+            const uint32_t base = (uint32_t)__cvta_generic_to_shared(&part);
+            const int n = parts * a.top;
+            unsigned long long mine = 0;
+            if ((int)threadIdx.x < n)                                       // (8 parts of 32: one each)
+                mine = ld_peer64(peer(base + (uint32_t)offsetof(LpPart, list) + 8u * (threadIdx.x % a.top),
+                                      threadIdx.x / a.top));
+            float pm = -INFINITY, pS = 0.0f, pA = 0.0f;
+            int pn = 0;
+            if (threadIdx.x < 32) {
+                if (lane < parts) {
+                    pm = __uint_as_float(ld_peer32(peer(base + (uint32_t)offsetof(LpPart, m), lane)));
+                    pS = __uint_as_float(ld_peer32(peer(base + (uint32_t)offsetof(LpPart, S), lane)));
+                    pA = __uint_as_float(ld_peer32(peer(base + (uint32_t)offsetof(LpPart, A), lane)));
+                    pn = (int)ld_peer32(peer(base + (uint32_t)offsetof(LpPart, nan), lane));
+                }
+                float all = pm;
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+                if (all > -INFINITY) {
+                    const float dt = fmaxf((pm - all) * kLog2e, kTiny), c = exp2_fast(dt);
+                    pA = c * fmaf(pS, dt, pA);
+                    pS *= c;
+                }
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) {
+                    pS += __shfl_xor_sync(0xffffffffu, pS, o);
+                    pA += __shfl_xor_sync(0xffffffffu, pA, o);
+                }
+                pn = __any_sync(0xffffffffu, pn);
+                pm = all;
+            }
+            __syncthreads();                                                // part is read by this CTA too
+            if ((int)threadIdx.x < n) cand[threadIdx.x] = mine;
+            if (threadIdx.x == 0) { part.m = pm; part.S = pS; part.A = pA; part.nan = pn; }
+            __syncthreads();
+            if (mine != 0) {
+                int before = 0;
+                for (int o = 0; o < n; ++o) before += cand[o] > mine;
+                if (before < a.top) part.list[before] = mine;
+            }
+            __syncthreads();
         }
-        for (int o = 16; o > 0; o >>= 1) {
-            const unsigned long long c = __shfl_xor_sync(0xffffffffu, best, o);
-            best = c > best ? c : best;
-        }
-        __syncthreads();
-        if (lane == 0) kred[warp] = best;
-        __syncthreads();
-        for (int w = 0; w < kLpThreads / 32; ++w) best = kred[w] > best ? kred[w] : best;
-        last = best;
-        if (threadIdx.x == 0) {
-            const int i = (int)(0xffffffffu - (uint32_t)best);
-            a.top_id[row * a.top + k] = i;
-            a.top_logprob[row * a.top + k] = logprob(X::get(x[i]));
-        }
+        cluster_sync();                                                     // (the others' parts have been read)
+        if (rank != 0) return;
     }
+
+    const float rm = part.m;
+    const bool bad = part.nan || rm == INFINITY, empty = !bad && rm == -INFINITY;
+    const float logS = logf(part.S);
+    auto logprob = [&](float v) { return bad ? NAN : empty ? -INFINITY : (v - rm) - logS; };
+    if (threadIdx.x == 0) {
+        if (a.entropy) a.entropy[row] = bad ? NAN : empty ? 0.0f : logS - part.A * kLn2 / part.S;
+        if (a.tokens) a.logprob[row] = tok < 0 ? 0.0f : tok >= a.vocab ? NAN : logprob(tok_x);
+    }
+    if ((int)threadIdx.x < a.top) {
+        const unsigned long long e = part.list[threadIdx.x];
+        a.top_id[row * a.top + threadIdx.x] = entry_index(e);
+        a.top_logprob[row * a.top + threadIdx.x] = logprob(key_value((uint32_t)(e >> 32)));
+    }
+}
+
+// CTAs of a row: enough for two per SM, parts of at least 2048 logits.
+int row_parts(int64_t rows, int64_t vocab, int sms) {
+    int parts = 1;
+    while (parts < kLpCluster && rows * parts < 2 * sms && vocab / (parts * 2) >= 2048) parts *= 2;
+    return parts;
+}
+
+template <int DT>
+cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, int sms, cudaStream_t s) {
+    const int parts = row_parts(rows, a.vocab, sms);
+    if (parts == 1) {
+        logprobs_kernel<DT, false><<<(unsigned)rows, kLpThreads, 0, s>>>(a, 1);
+        return cudaGetLastError();
+    }
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)parts;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * parts));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, true>, a, parts);
 }
 
 }  // namespace
@@ -125,8 +464,13 @@ extern "C" lb_status lb_token_logprobs(const void* logits, lb_dtype dtype, int64
         return LB_ERR_ALIGNMENT;
     const lb_status st = dense_device_ok();
     if (st != LB_OK) return st;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return LB_ERR_CUDA;
     const LogprobArgs a = {logits, tokens, logprob, entropy, top_id, top_logprob, ld, (int)vocab, top};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    with_dtype(dtype, [&](auto d) { logprobs_kernel<d.value><<<(unsigned)rows, kLpThreads, 0, s>>>(a); });
-    return cudaGetLastError() == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+    const cudaError_t e =
+        with_dtype(dtype, [&](auto d) { return launch_logprobs<d.value>(a, rows, sms, s); });
+    return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
 }

@@ -55,33 +55,6 @@ constexpr float kLow = 1e-30f, kHigh = 1e30f;
 
 constexpr int kMaxThreads = 1024;
 
-// Two fp32 at a time: sm_100 issues one instruction for both.
-struct F2 { unsigned long long u; };
-__device__ __forceinline__ F2 f2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 halves(F2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v.u));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-    return r;
-}
 // max(m, |v.x|, |v.y|); NaN if one is.
 __device__ __forceinline__ float max_abs(float m, F2 v) {
     const float2 h = halves(v);
@@ -93,59 +66,6 @@ __device__ __forceinline__ float max_abs(float m, F2 v) {
 // With this many rows or fewer a row takes four times the threads (8 elements each
 // instead of 32): its latency is what the call waits for.
 constexpr int64_t kFewRows = 148;
-
-// The VE elements of a 16-byte piece as pairs, and back.
-template <int DT> struct Piece;
-template <> struct Piece<LB_F32> {
-    static constexpr int VE = 4;
-    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[2]) {
-        v[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
-        v[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
-    }
-    static __device__ __forceinline__ uint4 pack(const F2 (&v)[2]) {
-        const float2 a = halves(v[0]), b = halves(v[1]);
-        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
-    }
-};
-template <> struct Piece<LB_BF16> {
-    static constexpr int VE = 8;
-    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[4]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-    }
-    static __device__ __forceinline__ uint4 pack(const F2 (&v)[4]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 h = halves(v[i]);
-            const __nv_bfloat162 b = __floats2bfloat162_rn(h.x, h.y);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-template <> struct Piece<LB_F16> {
-    static constexpr int VE = 8;
-    static __device__ __forceinline__ void unpack(uint4 u, F2 (&v)[4]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            v[i] = f2(f.x, f.y);
-        }
-    }
-    static __device__ __forceinline__ uint4 pack(const F2 (&v)[4]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 h = halves(v[i]);
-            const __half2 b = __floats2half2_rn(h.x, h.y);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
 
 // The piece at p, n of its elements inside the row (the rest 0).  VEC: 16
 // consecutive bytes; otherwise (pointers or pitches that are not multiples of
