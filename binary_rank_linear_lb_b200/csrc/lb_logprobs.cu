@@ -12,11 +12,10 @@
 // them (about 5 an element) close behind for 16-bit logits.
 //
 // The alternatives need no second pass either: the threads' maxima bound them.
-// If T is the top-th largest of the maxima, at least `top` logits are >= T, so
-// the alternatives are among the logits >= T, and only threads whose maximum is
-// >= T hold any: those few read their pieces again (from L2).  T is found by
-// bisection over the maxima (any bound with `top` maxima above it will do), the
-// candidates are ranked by counting.  Where many logits equal T (a mask that leaves
+// If `top` of the maxima of 64 groups of threads are >= T, the alternatives are
+// among the logits >= T, and only threads whose maximum is >= T hold any: those
+// few pieces are read again (from L2).  T is found by bisection over the groups'
+// maxima, the candidates are ranked by counting.  Where many logits equal T (a mask that leaves
 // few) only the first of those are taken; rows where too many lie above it, or
 // with a NaN, take `top` rounds of a maximum instead.
 //
@@ -32,6 +31,7 @@ namespace {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;
+constexpr int kGroups = 64;                  // groups of four threads
 constexpr int kCandidates = 1024;            // logits >= T kept at most
 constexpr int kLpCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -114,6 +114,17 @@ struct Stat {
     }
 };
 
+// Entries of cand[0 .. n) that come before `mine`.
+__device__ __forceinline__ int rank_of(unsigned long long mine, const unsigned long long* cand, int n) {
+    int before = 0, o = 0;
+#pragma unroll 4
+    for (; o + 1 < n; o += 2) {
+        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cand + o);
+        before += (c.x > mine) + (c.y > mine);
+    }
+    return o < n ? before + (cand[o] > mine) : before;
+}
+
 // What a CTA knows of its part of a row.
 struct LpPart {
     float m, S, A;
@@ -150,9 +161,9 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
     constexpr int VE = Piece<DT>::VE;
     constexpr int kBatch = 16 / VE;                // pieces of a batch: 16 logits
     __shared__ float fred[2][kLpWarps];
-    __shared__ uint32_t kmax[kLpWarps], kmin[kLpWarps];
+    __shared__ __align__(8) uint32_t group[kGroups];
     __shared__ int n_cand;
-    __shared__ unsigned long long cand[kCandidates];
+    __shared__ __align__(16) unsigned long long cand[kCandidates];
     __shared__ LpPart part;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = SPLIT ? (int)(blockIdx.x % parts) : 0;
@@ -184,16 +195,19 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
     };
 
     Stat st;
-    for (int j = p0 + (int)threadIdx.x; j < p1; j += kBatch * kLpThreads) {
-        uint4 raw[kBatch];
+    uint4 raw[kBatch];                             // the next batch is requested before one is taken
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) raw[b] = load(j + b * kLpThreads);
+    for (int b = 0; b < kBatch; ++b) raw[b] = load(p0 + (int)threadIdx.x + b * kLpThreads);
+    for (int j = p0 + (int)threadIdx.x; j < p1; j += kBatch * kLpThreads) {
         F2 v[8];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             F2 (&vb)[VE / 2] = *reinterpret_cast<F2 (*)[VE / 2]>(&v[b * VE / 2]);
             Piece<DT>::unpack(raw[b], vb);
         }
+        if (j + kBatch * kLpThreads < p1)
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) raw[b] = load(j + (kBatch + b) * kLpThreads);
         st.take(v);
     }
 
@@ -201,14 +215,14 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
     const bool some = p0 + (int)threadIdx.x < p1;            // this thread holds logits
     const uint32_t key = some ? order_key(st.m) : 0u;
     {
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, key);
-        const uint32_t lo = __reduce_min_sync(0xffffffffu, some ? key : 0xffffffffu);
-        if (lane == 0) { kmax[warp] = hi; kmin[warp] = lo; }
+        // maxima of four threads each, which bound the alternatives, and the row's
+        uint32_t g = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+        g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
+        if ((lane & 3) == 0) group[threadIdx.x / 4] = g;
     }
     const bool nan = __syncthreads_or(st.nan) != 0;
-    uint32_t hi = 0, lo = 0xffffffffu;
-#pragma unroll
-    for (int w = 0; w < kLpWarps; ++w) { hi = max(hi, kmax[w]); lo = min(lo, kmin[w]); }
+    const uint2 mine2 = *reinterpret_cast<const uint2*>(&group[2 * lane]);   // two groups a lane
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, max(mine2.x, mine2.y));
     const float M = hi ? key_value(hi) : -INFINITY;
     float S = halves(st.S).x + halves(st.S).y, A = halves(st.A).x + halves(st.A).y;
     if (M > -INFINITY) {
@@ -227,14 +241,20 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
         const int held = (n_pieces < p1 ? n_pieces : p1) - p0;             // pieces of this part
         bool rounds = nan;
         if (!rounds) {
-            // T: at least `top` of the threads' maxima are >= T (0: every logit is a candidate)
+            // T: at least `top` of the groups' maxima are >= T (0: every logit is a
+            // candidate).  Every warp bisects on its own; any T with `top` to
+            // top * 5 / 4 + 1 maxima above it will do.
             uint32_t T0 = 0;
-            if (held >= a.top && kLpThreads >= a.top) {
-                T0 = lo;
-                uint32_t end = hi;                                         // T0 <= T < end + 1
+            bool tied = false;                     // most groups share the lowest maximum
+            const int full = ((held < kLpThreads ? held : kLpThreads) + 3) / 4;   // groups with logits
+            if (full >= a.top) {
+                const uint32_t a0 = mine2.x ? mine2.x : 0xffffffffu, a1 = mine2.y ? mine2.y : 0xffffffffu;
+                const uint32_t lo = T0 = __reduce_min_sync(0xffffffffu, min(a0, a1));
+                uint32_t end = hi;
                 while (T0 < end) {
                     const uint32_t mid = T0 + (end - T0 + 1) / 2;
-                    const int c = __syncthreads_count(some && key >= mid);
+                    const int c = __popc(__ballot_sync(0xffffffffu, mine2.x >= mid)) +
+                                  __popc(__ballot_sync(0xffffffffu, mine2.y >= mid));
                     if (c >= a.top) {
                         T0 = mid;
                         if (c <= a.top + a.top / 4 + 1) break;
@@ -242,19 +262,30 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
                         end = mid - 1;
                     }
                 }
+                tied = T0 == lo && full > a.top + a.top / 4 + 1;
             }
-            // the logits >= from that the threads with a maximum >= from hold
+            // The logits >= from that the threads with a maximum >= from hold.  The warp
+            // reads such a thread's pieces together, a lane each, for kTogether
+            // threads at a time: one round trip to L2 instead of one per batch.
+            constexpr int kTogether = 4;
             auto gather = [&](uint32_t from) {
-                if (some && key >= from)
-                    for (int j = p0 + (int)threadIdx.x; j < p1; j += kBatch * kLpThreads) {
-                        uint4 raw[kBatch];
+                uint32_t who = __ballot_sync(0xffffffffu, some && key >= from);
+                while (who) {
+                    int j0[kTogether];
 #pragma unroll
-                        for (int b = 0; b < kBatch; ++b) raw[b] = load(j + b * kLpThreads);
+                    for (int w = 0; w < kTogether; ++w) {
+                        j0[w] = who ? p0 + warp * 32 + __ffs(who) - 1 + lane * kLpThreads : p1;
+                        who &= who - 1;
+                    }
+                    for (int off = 0; p0 + warp * 32 + off < p1; off += 32 * kLpThreads) {
+                        uint4 r[kTogether];
 #pragma unroll
-                        for (int b = 0; b < kBatch; ++b) {
-                            const T* e = reinterpret_cast<const T*>(&raw[b]);
-                            const int i = (j + b * kLpThreads) * VE - shift;
-                            if (j + b * kLpThreads >= p1) break;
+                        for (int w = 0; w < kTogether; ++w) r[w] = load(j0[w] + off);
+#pragma unroll
+                        for (int w = 0; w < kTogether; ++w) {
+                            const int j = j0[w] + off, i = j * VE - shift;
+                            if (j >= p1) continue;
+                            const T* e = reinterpret_cast<const T*>(&r[w]);
 #pragma unroll
                             for (int k = 0; k < VE; ++k) {
                                 const uint32_t ek = order_key(X::get(e[k]));
@@ -265,10 +296,11 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
                             }
                         }
                     }
+                }
                 __syncthreads();
             };
-            gather(T0);
-            if (n_cand > kCandidates) {
+            if (!tied) gather(T0);
+            if (tied || n_cand > kCandidates) {
                 // Many equal T (a mask that leaves few, a constant row): take those above
                 // it, and the first of the equal ones as a warp meets them in order.
                 __syncthreads();
@@ -308,8 +340,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
             const int n = n_cand;
             for (int c = threadIdx.x; c < n; c += kLpThreads) {
                 const unsigned long long mine = cand[c];
-                int before = 0;
-                for (int o = 0; o < n; ++o) before += cand[o] > mine;
+                const int before = rank_of(mine, cand, n);
                 if (before < a.top) part.list[before] = mine;
             }
             if ((int)threadIdx.x >= n && (int)threadIdx.x < a.top) part.list[threadIdx.x] = 0;
@@ -390,8 +421,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
             if (threadIdx.x == 0) { part.m = pm; part.S = pS; part.A = pA; part.nan = pn; }
             __syncthreads();
             if (mine != 0) {
-                int before = 0;
-                for (int o = 0; o < n; ++o) before += cand[o] > mine;
+                const int before = rank_of(mine, cand, n);
                 if (before < a.top) part.list[before] = mine;
             }
             __syncthreads();
