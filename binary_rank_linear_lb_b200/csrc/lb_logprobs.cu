@@ -194,20 +194,56 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
         return u;
     };
 
+    // This thread's pieces are p0 + threadIdx.x + k * kLpThreads.  Those of a first
+    // step that holds the row's partial first piece, and of the last batch, are
+    // checked one by one; the batches between are whole for every thread.
     Stat st;
-    uint4 raw[kBatch];                             // the next batch is requested before one is taken
+    int k = 0;
+    auto step = [&] {
+        const int j = p0 + (int)threadIdx.x + k * kLpThreads;
+        if (j < p1) {
+            F2 v[VE / 2];
+            Piece<DT>::unpack(load(j), v);
+            st.take(v);
+        }
+        ++k;
+    };
+    if (shift > 0 && p0 == 0) step();
+    const int whole = min(p1, (shift + a.vocab) / VE);       // pieces below it end inside the row
+    int batches = (whole - p0 - k * kLpThreads) / (kBatch * kLpThreads);
+    if (batches > 0) {
+        const uint4* p = reinterpret_cast<const uint4*>(x - shift) + p0 + threadIdx.x + k * kLpThreads;
+        k += batches * kBatch;
+        uint4 raw[kBatch];                         // the next batch is requested before one is taken
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) raw[b] = load(p0 + (int)threadIdx.x + b * kLpThreads);
-    for (int j = p0 + (int)threadIdx.x; j < p1; j += kBatch * kLpThreads) {
+        for (int b = 0; b < kBatch; ++b) raw[b] = __ldg(p + b * kLpThreads);
+        while (true) {
+            F2 v[8];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                F2 (&vb)[VE / 2] = *reinterpret_cast<F2 (*)[VE / 2]>(&v[b * VE / 2]);
+                Piece<DT>::unpack(raw[b], vb);
+            }
+            p += kBatch * kLpThreads;
+            if (--batches > 0)
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) raw[b] = __ldg(p + b * kLpThreads);
+            st.take(v);
+            if (batches == 0) break;
+        }
+    }
+    for (; p0 + k * kLpThreads < p1; k += kBatch) {
+        const int j = p0 + (int)threadIdx.x + k * kLpThreads;
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) raw[b] = load(j + b * kLpThreads);
+        if (j >= p1) break;
         F2 v[8];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             F2 (&vb)[VE / 2] = *reinterpret_cast<F2 (*)[VE / 2]>(&v[b * VE / 2]);
             Piece<DT>::unpack(raw[b], vb);
         }
-        if (j + kBatch * kLpThreads < p1)
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) raw[b] = load(j + (kBatch + b) * kLpThreads);
         st.take(v);
     }
 
@@ -265,33 +301,39 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
                 tied = T0 == lo && full > a.top + a.top / 4 + 1;
             }
             // The logits >= from that the threads with a maximum >= from hold.  The warp
-            // reads such a thread's pieces together, a lane each, for kTogether
-            // threads at a time: one round trip to L2 instead of one per batch.
-            constexpr int kTogether = 4;
+            // reads such a thread's pieces together, a lane each (kTogether threads at a
+            // time): one round trip to L2 instead of one per batch.
+            constexpr int kTogether = 2;
             auto gather = [&](uint32_t from) {
+                const float value = from == 0 ? -INFINITY : key_value(from);
                 uint32_t who = __ballot_sync(0xffffffffu, some && key >= from);
                 while (who) {
-                    int j0[kTogether];
-#pragma unroll
-                    for (int w = 0; w < kTogether; ++w) {
-                        j0[w] = who ? p0 + warp * 32 + __ffs(who) - 1 + lane * kLpThreads : p1;
-                        who &= who - 1;
-                    }
-                    for (int off = 0; p0 + warp * 32 + off < p1; off += 32 * kLpThreads) {
+                    const int l0 = __ffs(who) - 1;
+                    who &= who - 1;
+                    const int l1 = who ? __ffs(who) - 1 : -1;
+                    who &= who - 1;
+                    for (int off = p0 + warp * 32 + lane * kLpThreads; off - lane * kLpThreads < p1;
+                         off += 32 * kLpThreads) {
                         uint4 r[kTogether];
-#pragma unroll
-                        for (int w = 0; w < kTogether; ++w) r[w] = load(j0[w] + off);
+                        r[0] = load(off + l0);
+                        if (l1 >= 0) r[1] = load(off + l1);
 #pragma unroll
                         for (int w = 0; w < kTogether; ++w) {
-                            const int j = j0[w] + off, i = j * VE - shift;
-                            if (j >= p1) continue;
+                            if (w == 1 && l1 < 0) break;
+                            const int j = off + (w ? l1 : l0), i = j * VE - shift;
+                            F2 v[VE / 2];
+                            Piece<DT>::unpack(r[w], v);
+                            float top = -INFINITY;
+#pragma unroll
+                            for (int q = 0; q < VE / 2; ++q) top = max3_nan(top, v[q]);
+                            if (j >= p1 || top < value) continue;
                             const T* e = reinterpret_cast<const T*>(&r[w]);
 #pragma unroll
-                            for (int k = 0; k < VE; ++k) {
-                                const uint32_t ek = order_key(X::get(e[k]));
-                                if (ek >= from && i + k >= 0 && i + k < a.vocab) {
+                            for (int q = 0; q < VE; ++q) {
+                                const uint32_t ek = order_key(X::get(e[q]));
+                                if (ek >= from && i + q >= 0 && i + q < a.vocab) {
                                     const int at = atomicAdd(&n_cand, 1);
-                                    if (at < kCandidates) cand[at] = entry_of(ek, i + k);
+                                    if (at < kCandidates) cand[at] = entry_of(ek, i + q);
                                 }
                             }
                         }
