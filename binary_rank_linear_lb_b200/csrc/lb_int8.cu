@@ -75,6 +75,111 @@ __global__ void __launch_bounds__(256) int8_general_kernel(const Int8Args a) {
     }
 }
 
+// ------------------------------------------------------------ few tokens
+// One to four tokens: the weights stream past once and __dp4a keeps up (M products
+// of four per weight word, against 64 a clock and SM).  A warp takes four
+// channels and, with few channels, a block's warps share their K (`parts`), so
+// that every SM has some 100 KB of weights in flight; a lane holds 16 bytes of
+// every row, 512 contiguous bytes a warp.  xq comes from L1.
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewCh = 4;                          // channels of a warp
+constexpr int kFewTok = 4;                         // tokens at most
+
+__device__ __forceinline__ int dot16(int4 a, int4 b, int acc) {
+    acc = __dp4a(a.x, b.x, acc);
+    acc = __dp4a(a.y, b.y, acc);
+    acc = __dp4a(a.z, b.z, acc);
+    return __dp4a(a.w, b.w, acc);
+}
+__device__ __forceinline__ int4 ld_once(const int8_t* p) {
+    int4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+template <int DT, int MT>
+__global__ void __launch_bounds__(kFewThreads) int8_few_kernel(const __grid_constant__ Int8Args a, int parts) {
+    using Y = Elem<DT>;
+    __shared__ int part_sums[kFewWarps][kFewCh * MT];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = warp % parts;
+    const int64_t n0 = ((int64_t)blockIdx.x * (kFewWarps / parts) + warp / parts) * kFewCh;
+    const int chunks = a.K / 16;                   // whole 16-byte chunks of a row
+    const int c0 = (int)((int64_t)chunks * part / parts), c1 = (int)((int64_t)chunks * (part + 1) / parts);
+    int acc[kFewCh][MT] = {};
+    const int8_t* w[kFewCh];
+    const int8_t* x[MT];
+#pragma unroll
+    for (int i = 0; i < kFewCh; ++i) w[i] = a.w + (n0 + i < a.N ? n0 + i : a.N - 1) * a.ldw;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x[m] = a.x + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
+    constexpr int kAhead = 2;                      // chunks requested together
+    int c = c0 + lane;
+    for (; c + 32 * (kAhead - 1) < c1; c += 32 * kAhead) {
+        int4 wv[kAhead][kFewCh];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int i = 0; i < kFewCh; ++i) wv[u][i] = ld_once(w[i] + 16 * (int64_t)(c + 32 * u));
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int4 xv = __ldg(reinterpret_cast<const int4*>(x[m]) + c + 32 * u);
+#pragma unroll
+                for (int i = 0; i < kFewCh; ++i) acc[i][m] = dot16(wv[u][i], xv, acc[i][m]);
+            }
+    }
+    for (; c < c1; c += 32)
+#pragma unroll
+        for (int i = 0; i < kFewCh; ++i) {
+            const int4 wv = ld_once(w[i] + 16 * (int64_t)c);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[i][m] = dot16(wv, __ldg(reinterpret_cast<const int4*>(x[m]) + c), acc[i][m]);
+        }
+    if (part == parts - 1 && lane < a.K - 16 * chunks)           // the last bytes, one a lane
+#pragma unroll
+        for (int i = 0; i < kFewCh; ++i)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[i][m] += (int)w[i][16 * chunks + lane] * (int)x[m][16 * chunks + lane];
+#pragma unroll
+    for (int i = 0; i < kFewCh; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[i][m] = __reduce_add_sync(0xffffffffu, acc[i][m]);
+    // lane (i, m) of the group's first warp stores channel n0 + i of token m
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kFewCh; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) if (lane == m * kFewCh + i) sum = acc[i][m];
+    if (parts > 1) {
+        if (lane < kFewCh * MT) part_sums[warp][lane] = sum;
+        __syncthreads();
+        if (part != 0) return;
+        if (lane < kFewCh * MT)
+            for (int p = 1; p < parts; ++p) sum += part_sums[warp + p][lane];
+    }
+    const int m = lane / kFewCh;
+    const int64_t n = n0 + lane % kFewCh;
+    if (lane < kFewCh * MT && m < a.M && n < a.N)
+        static_cast<typename Y::T*>(a.y)[(int64_t)m * a.ldy + n] = Y::put((float)sum * a.xs[m] * a.ws[n]);
+}
+
+template <int DT>
+cudaError_t launch_few(const Int8Args& a, int sms, cudaStream_t s) {
+    const int64_t groups = ((int64_t)a.N + kFewCh - 1) / kFewCh;
+    int parts = 1;
+    while (parts < kFewWarps && groups * parts < (int64_t)sms * 24 && a.K / (parts * 2) >= 1024) parts *= 2;
+    const int per_block = kFewWarps / parts;
+    const unsigned blocks = (unsigned)((groups + per_block - 1) / per_block);
+    if (a.M == 1) int8_few_kernel<DT, 1><<<blocks, kFewThreads, 0, s>>>(a, parts);
+    else if (a.M == 2) int8_few_kernel<DT, 2><<<blocks, kFewThreads, 0, s>>>(a, parts);
+    else int8_few_kernel<DT, 4><<<blocks, kFewThreads, 0, s>>>(a, parts);
+    return cudaGetLastError();
+}
+
 // ------------------------------------------------------------ tensor cores
 // y^T tile = (128 channels of wq) x (nt tokens of xq): tcgen05.mma kind::i8, the
 // weights as A, the tokens as B, int32 accumulators in TMEM.  The channels are
@@ -103,8 +208,10 @@ constexpr int kMaxTok = 256;                       // tokens of a tile at most
 constexpr int kKBytes = 128;                       // K per stage
 constexpr int kWBytes = kTileCh * kKBytes;         // 16 KB
 constexpr int kMaxStages8 = 12;
-constexpr int kPipeBytes = 216 * 1024;             // stages (and a split's partial sums)
-constexpr int kMaxSplit8 = 8;
+constexpr int kPipeBytes = 216 * 1024;             // stages; then a split's partial sums
+static_assert(kTileCh * (kMaxTok + 4) * 4 <= kPipeBytes, "partial sums");
+constexpr int kMaxLgSplit = 3;                     // at most 8 CTAs share a tile
+constexpr int kMaxSplit8 = 1 << kMaxLgSplit;
 constexpr long long kWaitLimit8 = 4000000000LL;    // cycles (~2 s)
 
 struct Ctl8 {
@@ -120,7 +227,7 @@ struct MmaPlan {
     int nt;               // tokens per tile, a multiple of 16
     int n_tok, n_ch;      // tiles along the tokens and the channels
     int n_kb;             // K blocks
-    int split;            // CTAs of the cluster that share a tile's K blocks
+    int lg_split;         // log2 of the CTAs that share a tile's K blocks
     int stages, stage_bytes;
     int acc_cols;         // columns of one accumulator, a multiple of 32
     int tmem_cols;        // allocated: a power of two >= 2 acc_cols
@@ -128,25 +235,26 @@ struct MmaPlan {
 
 __device__ __forceinline__ uint32_t s32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ bool wait8(Ctl8* c, uint64_t* bar, uint32_t parity) {
-    const uint32_t a = s32(bar);
-    if (mbar_try_wait(a, parity)) return true;
+__device__ __noinline__ bool wait8_slow(volatile int* abort, uint32_t bar, uint32_t parity) {
     const long long t0 = clock64();
     while (true) {
-        if (mbar_try_wait(a, parity)) return true;
-        if (*reinterpret_cast<volatile int*>(&c->abort)) return false;
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
         if (clock64() - t0 > kWaitLimit8) {
-            atomicExch(&c->abort, 1);
+            *abort = 1;
             return false;
         }
     }
 }
+// Waits for a barrier's phase; false when it gave up (bounded, about 2 s).
+__device__ __forceinline__ bool wait8(Ctl8* c, uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait8_slow(&c->abort, bar, parity);
+}
 
 // Shared-memory descriptor: K-major, 128-byte swizzle, 8-row atoms of 1024 bytes.
-__device__ __forceinline__ uint64_t desc8(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-           (2ull << 61);
-}
+// The low word holds the address in 16-byte units.
+constexpr uint64_t kDesc8 = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ uint64_t desc8(uint32_t saddr) { return kDesc8 | ((saddr & 0x3FFFFu) >> 4); }
 // Instruction descriptor of kind::i8: int32 accumulator, signed A and B, both K-major.
 __device__ __forceinline__ uint32_t idesc8(int m, int n) {
     return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
@@ -181,19 +289,21 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, int (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void cluster_sync8() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive8() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t cluster_rank8() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+__device__ __forceinline__ void cluster_wait8() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Address of the same shared variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr8(uint32_t addr, uint32_t rank) {
     uint32_t p;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
     return p;
+}
+__device__ __forceinline__ void st_cluster8(uint32_t addr, int a, int b, int c, int d) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
+                 :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void st_cluster8(uint32_t addr, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
@@ -210,149 +320,190 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
     unsigned char* basep = dsm + (base - raw);
     Ctl8* ctl = reinterpret_cast<Ctl8*>(basep + kPipeBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = SPLIT ? (int)cluster_rank8() : 0;
-    const int parts = SPLIT ? p.split : 1;
-    const int first = (int)blockIdx.x / parts, step = (int)gridDim.x / parts;
-    const int n_tiles = p.n_tok * p.n_ch;
-    const int kb0 = (int)((long long)p.n_kb * rank / parts);
-    const int kb1 = (int)((long long)p.n_kb * (rank + 1) / parts);
+    const int lg = SPLIT ? p.lg_split : 0;         // a cluster has 2^lg CTAs
+    const int rank = SPLIT ? (int)(blockIdx.x & ((1u << lg) - 1u)) : 0;
+    const int first = (int)(blockIdx.x >> lg), step = (int)(gridDim.x >> lg);
+    const int n_tok = p.n_tok, n_tiles = n_tok * p.n_ch, nt = p.nt;
+    const int kb0 = (p.n_kb * rank) >> lg, kb1 = (p.n_kb * (rank + 1)) >> lg;
+    const int stages = p.stages;
+    const uint32_t stage_bytes = (uint32_t)p.stage_bytes;
+    const uint32_t full = s32(&ctl->full[0]), empty = s32(&ctl->empty[0]);
+    const uint32_t acc_full = s32(&ctl->acc_full[0]), acc_empty = s32(&ctl->acc_empty[0]);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(s32(&ctl->full[s]), 1);
-            mbar_init(s32(&ctl->empty[s]), 1);
+    // The loading thread sets up the stages' barriers and requests the first stages
+    // before anything else; TMEM and the other barriers follow meanwhile.
+    int ls = 0, lkb = kb0, lt = first;             // its position: stage, K block, tile
+    uint32_t lph = 1;                              // a fresh stage counts as empty
+    int lc = (first / n_tok) * kTileCh, lm = (first % n_tok) * nt;
+    auto load_stage = [&] {
+        const uint32_t fb = full + 8u * (uint32_t)ls, sb = base + (uint32_t)ls * stage_bytes;
+        mbar_expect_tx(fb, stage_bytes);
+        tma_load_2d(sb, &wmap, fb, lkb * kKBytes, lc);
+        tma_load_2d(sb + kWBytes, &xmap, fb, lkb * kKBytes, lm);
+        if (++ls == stages) { ls = 0; lph ^= 1; }
+        if (++lkb == kb1) {
+            lkb = kb0;
+            lt += step;
+            lc = (lt / n_tok) * kTileCh;
+            lm = (lt % n_tok) * nt;
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(s32(&ctl->acc_full[i]), 1);
-            mbar_init(s32(&ctl->acc_empty[i]), kDrainWarps);
+    };
+    if (warp == kLoadWarp && lane == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full + 8u * s, 1);
+            mbar_init(empty + 8u * s, 1);
         }
-        ctl->abort = 0;
-        for (int r = 0; r < kMaxSplit8; ++r) ctl->lost[r] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int s = 0; s < stages && lt < n_tiles; ++s) load_stage();
     }
     if (warp == kIssueWarp) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(acc_full + 8u * i, 1);
+                mbar_init(acc_empty + 8u * i, kDrainWarps);
+            }
+            ctl->abort = 0;
+            for (int r = 0; r < kMaxSplit8; ++r) ctl->lost[r] = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      :: "r"(s32(&ctl->tmem_base)), "r"(p.tmem_cols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    __syncwarp();
     fence_before8();
     __syncthreads();
     fence_after8();
-    if (SPLIT) cluster_sync8();                    // every CTA of the cluster runs before one writes to it
     const uint32_t tmem = ctl->tmem_base;
 
     if (warp == kLoadWarp) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 1;                       // a fresh stage counts as empty
-            bool ok = true;
-            for (int t = first; t < n_tiles && ok; t += step) {
-                const int c0 = (t / p.n_tok) * kTileCh, m0 = (t % p.n_tok) * p.nt;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!(ok = wait8(ctl, &ctl->empty[s], ph))) break;
-                    const uint32_t fb = s32(&ctl->full[s]), sb = base + s * p.stage_bytes;
-                    mbar_expect_tx(fb, kWBytes + p.nt * kKBytes);
-                    tma_load_2d(sb, &wmap, fb, kb * kKBytes, c0);
-                    tma_load_2d(sb + kWBytes, &xmap, fb, kb * kKBytes, m0);
-                    if (++s == p.stages) { s = 0; ph ^= 1; }
-                }
-            }
-        }
+        if (lane == 0)
+            while (lt < n_tiles && wait8(ctl, empty + 8u * (uint32_t)ls, lph)) load_stage();
     } else if (warp == kIssueWarp) {
         if (lane == 0) {
-            const uint32_t id = idesc8(kTileCh, p.nt);
+            const uint32_t id = idesc8(kTileCh, nt);
+            const uint32_t acc_cols = (uint32_t)p.acc_cols;
             int s = 0, tl = 0;
-            uint32_t ph = 0;
+            uint32_t ph = 0, sb = base;
             bool ok = true;
             for (int t = first; t < n_tiles && ok; t += step, ++tl) {
-                const int buf = tl & 1;
-                if (!(ok = wait8(ctl, &ctl->acc_empty[buf], ((tl >> 1) & 1) ^ 1))) break;
+                const uint32_t buf = tl & 1;
+                if (!(ok = wait8(ctl, acc_empty + 8u * buf, ((tl >> 1) & 1) ^ 1))) break;
                 fence_after8();
-                const uint32_t d = tmem + (uint32_t)(buf * p.acc_cols);
+                const uint32_t d = tmem + buf * acc_cols;
+                uint32_t add = 0;                  // the tile's first product starts the sums
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!(ok = wait8(ctl, &ctl->full[s], ph))) break;
+                    if (!(ok = wait8(ctl, full + 8u * (uint32_t)s, ph))) break;
                     fence_after8();
-                    const uint32_t sb = base + s * p.stage_bytes;
                     const uint64_t ad = desc8(sb), bd = desc8(sb + kWBytes);
-#pragma unroll
-                    for (int kk = 0; kk < kKBytes / 32; ++kk)
-                        mma_i8(d, ad + 2ull * kk, bd + 2ull * kk, id, (kb != kb0) || kk != 0);
-                    commit8(s32(&ctl->empty[s]));
-                    if (++s == p.stages) { s = 0; ph ^= 1; }
+                    mma_i8(d, ad, bd, id, add);
+                    mma_i8(d, ad + 2, bd + 2, id, 1);
+                    mma_i8(d, ad + 4, bd + 4, id, 1);
+                    mma_i8(d, ad + 6, bd + 6, id, 1);
+                    add = 1;
+                    commit8(empty + 8u * (uint32_t)s);
+                    sb += stage_bytes;
+                    if (++s == stages) { s = 0; ph ^= 1; sb = base; }
                 }
-                if (ok) commit8(s32(&ctl->acc_full[buf]));
+                if (ok) commit8(acc_full + 8u * buf);
             }
         }
     } else {
         const int q = warp & 3, hw = warp >> 2;    // accumulator lanes 32q .. 32q + 31
         int tl = 0;
         for (int t = first; t < n_tiles; t += step, ++tl) {
-            const int c0 = (t / p.n_tok) * kTileCh, m0 = (t % p.n_tok) * p.nt;
-            const int buf = tl & 1;
+            const int c0 = (t / n_tok) * kTileCh, m0 = (t % n_tok) * nt;
+            const uint32_t buf = tl & 1;
             const int n = c0 + q * 32 + lane;
-            const float ws = n < a.N ? __ldg(a.ws + n) : 0.0f;
+            float ws = n < a.N ? __ldg(a.ws + n) : 0.0f;
+            const int cols = min(nt, a.M - m0);
+            float xl = lane < cols - 32 * hw ? __ldg(a.xs + m0 + 32 * hw + lane) : 0.0f;
             // every lane waits; the warp goes on together (the TMEM loads are warp-wide)
-            const bool ok = __all_sync(0xffffffffu, wait8(ctl, &ctl->acc_full[buf], (tl >> 1) & 1));
+            const bool ok = __all_sync(0xffffffffu, wait8(ctl, acc_full + 8u * buf, (tl >> 1) & 1));
             fence_after8();
-            const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * p.acc_cols);
+            const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + buf * (uint32_t)p.acc_cols;
             if constexpr (SPLIT) {
-                // partial sums to the CTA that folds their tokens: [source][token][channel]
-                const int per = p.nt / parts;
-                const uint32_t red = base + p.stages * p.stage_bytes;
-                for (int j = 32 * hw; j < p.nt; j += 64) {
+                // Once every CTA of the cluster has its sums (its stages are free then),
+                // each gives the others their channels' partial sums: [source][channel]
+                // [token], a channel's row padded to an odd number of 16-byte pieces.
+                cluster_arrive8();
+                cluster_wait8();
+                const uint32_t per = (uint32_t)kTileCh >> lg;          // channels a CTA folds
+                const uint32_t ch = (uint32_t)(q * 32 + lane), pitch = 4u * (uint32_t)(nt + 4);
+                const uint32_t dst = peer_addr8(base + ((uint32_t)rank * per + (ch & (per - 1))) * pitch, ch >> (7 - lg));
+                for (int j = 32 * hw; j < nt; j += 64) {
                     int v[32];
                     __syncwarp();
                     if (ok) tmem_ld8(tacc + (uint32_t)j, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (j + i >= p.nt) break;
-                        const int dst = (j + i) / per, col = (j + i) % per;
-                        st_cluster8(peer_addr8(red + 4u * (uint32_t)((rank * per + col) * kTileCh + q * 32 + lane),
-                                               (uint32_t)dst), v[i]);
-                    }
+                    for (int i = 0; i < 32; i += 4)
+                        if (j + i < nt) st_cluster8(dst + 4u * (uint32_t)(j + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
-                if (!ok && lane < parts)
-                    st_cluster8(peer_addr8(s32(&ctl->lost[rank]), (uint32_t)lane), 1);
+                if (!ok && lane < (1 << lg)) st_cluster8(peer_addr8(s32(&ctl->lost[rank]), (uint32_t)lane), 1);
                 break;                             // (a split call has one tile per cluster)
             } else {
-            for (int j = 32 * hw; j < p.nt; j += 64) {
-                int v[32];
-                __syncwarp();
-                if (ok) tmem_ld8(tacc + (uint32_t)j, v);
-                const float xl = m0 + j + lane < a.M ? __ldg(a.xs + m0 + j + lane) : 0.0f;
-                typename Y::T* y = static_cast<typename Y::T*>(a.y) + (int64_t)(m0 + j) * a.ldy + n;
-                const int cols = min(min(32, p.nt - j), a.M - (m0 + j));
+                if (!ok) ws = __int_as_float(0x7fc00000);              // NaN: the sums are not there
+                for (int j = 32 * hw; j < cols; j += 64) {
+                    int v[32];
+                    __syncwarp();
+                    if (ok) tmem_ld8(tacc + (uint32_t)j, v);
+                    const float xn = lane < cols - (j + 64) ? __ldg(a.xs + m0 + j + 64 + lane) : 0.0f;
+                    typename Y::T* y = static_cast<typename Y::T*>(a.y) + (int64_t)(m0 + j) * a.ldy + n;
+                    const int64_t ldy = a.ldy;
+                    if (j + 32 <= cols && c0 + kTileCh <= a.N) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float xs = __shfl_sync(0xffffffffu, xl, i);
-                    if (i < cols && n < a.N) *y = Y::put(ok ? (float)v[i] * xs * ws : __int_as_float(0x7fc00000));
-                    y += a.ldy;
+                        for (int i = 0; i < 32; ++i)
+                            y[i * ldy] = Y::put((float)v[i] * __shfl_sync(0xffffffffu, xl, i) * ws);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float xs = __shfl_sync(0xffffffffu, xl, i);
+                            if (j + i < cols && n < a.N) y[i * ldy] = Y::put((float)v[i] * xs * ws);
+                        }
+                    }
+                    xl = xn;
                 }
-            }
-            fence_before8();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s32(&ctl->acc_empty[buf]));
+                fence_before8();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
             }
         }
     }
-    if (SPLIT) {
+    if constexpr (SPLIT) {
         __syncwarp();
-        cluster_sync8();                           // all partial sums have arrived
-        if (first < n_tiles && warp < kDrainWarps) {
-            const int c0 = (first / p.n_tok) * kTileCh, m0 = (first % p.n_tok) * p.nt;
-            const int per = p.nt / parts;
-            const int ch = threadIdx.x & (kTileCh - 1), n = c0 + ch;
-            const int* red = reinterpret_cast<const int*>(basep + p.stages * p.stage_bytes);
-            bool ok = true;
-            for (int r = 0; r < parts; ++r) ok = ok && ctl->lost[r] == 0;
-            const float ws = n < a.N ? __ldg(a.ws + n) : 0.0f;
-            for (int col = threadIdx.x / kTileCh; col < per; col += kDrainWarps * 32 / kTileCh) {
-                const int m = m0 + rank * per + col;
-                if (n >= a.N || m >= a.M) continue;
-                int v = 0;
-                for (int r = 0; r < parts; ++r) v += red[(r * per + col) * kTileCh + ch];
-                static_cast<typename Y::T*>(a.y)[(int64_t)m * a.ldy + n] =
-                    Y::put(ok ? (float)v * __ldg(a.xs + m) * ws : __int_as_float(0x7fc00000));
+        if (warp >= kDrainWarps) {                 // (the draining warps have been through this one)
+            cluster_arrive8();
+            cluster_wait8();
+        }
+        cluster_arrive8();
+        cluster_wait8();                           // all partial sums have arrived
+        if (warp < kDrainWarps) {
+            const int c0 = (first / n_tok) * kTileCh, m0 = (first % n_tok) * nt;
+            const int per = kTileCh >> lg, parts = 1 << lg;
+            const int ch = threadIdx.x & (per - 1), n = c0 + rank * per + ch;
+            const uint32_t pitch = 4u * (uint32_t)(nt + 4);
+            float ws = n < a.N ? __ldg(a.ws + n) : 0.0f;
+            for (int r = 0; r < parts; ++r)
+                if (ctl->lost[r]) ws = __int_as_float(0x7fc00000);
+            const int cols = min(nt, a.M - m0);
+            const int4* red = reinterpret_cast<const int4*>(basep + (uint32_t)ch * pitch);
+            const uint32_t part_step = (uint32_t)per * pitch / 16u;
+            for (int j = 4 * (int)(threadIdx.x >> (7 - lg)); j < cols; j += 4 * ((kDrainWarps * 32) >> (7 - lg))) {
+                float xs[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xs[i] = j + i < cols ? __ldg(a.xs + m0 + j + i) : 0.0f;
+                int4 v = red[j / 4];
+                for (int r = 1; r < parts; ++r) {
+                    const int4 o = red[(uint32_t)r * part_step + j / 4];
+                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                }
+                if (n >= a.N) continue;
+                typename Y::T* y = static_cast<typename Y::T*>(a.y) + (int64_t)(m0 + j) * a.ldy + n;
+                const int vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j + i < cols) y[i * a.ldy] = Y::put((float)vv[i] * xs[i] * ws);
             }
         }
     }
@@ -410,14 +561,12 @@ MmaPlan mma_plan(int64_t M, int64_t N, int64_t K, int sms) {
     p.n_tok = (int)((M + p.nt - 1) / p.nt);
     p.n_ch = (int)((N + kTileCh - 1) / kTileCh);
     p.n_kb = (int)((K + kKBytes - 1) / kKBytes);
-    p.split = 1;
     const int64_t tiles = (int64_t)p.n_tok * p.n_ch;
     // halve the K range while the clusters fit the SMs and a part keeps 4 blocks
-    while (p.split < kMaxSplit8 && tiles * p.split * 2 <= sms && p.n_kb / (p.split * 2) >= 4) p.split *= 2;
-    const int red = p.split > 1 ? kTileCh * p.nt * 4 : 0;
+    while (p.lg_split < kMaxLgSplit && (tiles << (p.lg_split + 1)) <= sms && (p.n_kb >> (p.lg_split + 1)) >= 4)
+        ++p.lg_split;
     p.stage_bytes = kWBytes + p.nt * kKBytes;
-    p.stages = (kPipeBytes - red) / p.stage_bytes;
-    if (p.stages > kMaxStages8) p.stages = kMaxStages8;
+    p.stages = std::min(kPipeBytes / p.stage_bytes, kMaxStages8);
     p.acc_cols = (p.nt + 31) / 32 * 32;
     p.tmem_cols = 64;
     while (p.tmem_cols < 2 * p.acc_cols) p.tmem_cols *= 2;
@@ -430,10 +579,10 @@ cudaError_t launch_mma(const Int8Args& a, const MmaPlan& p, const CUtensorMap& w
     const int64_t tiles = (int64_t)p.n_tok * p.n_ch;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)p.split;
+    at[0].val.clusterDim.x = 1u << p.lg_split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * p.split : std::min<int64_t>(tiles, sms)));
+    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles << p.lg_split : std::min<int64_t>(tiles, sms)));
     cfg.blockDim = dim3(kMmaThreads);
     cfg.dynamicSmemBytes = kMmaSmem;
     cfg.stream = s;
@@ -478,6 +627,10 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return LB_ERR_CUDA;
+        if (M <= kFewTok && (M <= 2 || in * out < (1 << 25)) && !getenv("NOFEW")) {
+            const cudaError_t e = with_dtype(y_dtype, [&](auto d) { return launch_few<d.value>(a, sms, s); });
+            return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+        }
         const MmaPlan p = mma_plan(M, out, in, sms);
         CUtensorMap wm, xm;
         // (the pitch of a single row is never used; the map wants a multiple of 16)
@@ -485,7 +638,7 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
             !code_map(&xm, xq, M, in, M == 1 ? (in + 15) / 16 * 16 : ldx, p.nt))
             return LB_ERR_CUDA;
         const cudaError_t e = with_dtype(y_dtype, [&](auto d) {
-            return p.split > 1 ? launch_mma<d.value, true>(a, p, wm, xm, sms, s)
+            return p.lg_split > 0 ? launch_mma<d.value, true>(a, p, wm, xm, sms, s)
                                : launch_mma<d.value, false>(a, p, wm, xm, sms, s);
         });
         return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
