@@ -266,6 +266,11 @@ __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
         :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
+__device__ __forceinline__ bool elect8() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
 __device__ __forceinline__ void commit8(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                  :: "r"(bar) : "memory");
@@ -381,33 +386,38 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
         if (lane == 0)
             while (lt < n_tiles && wait8(ctl, empty + 8u * (uint32_t)ls, lph)) load_stage();
     } else if (warp == kIssueWarp) {
-        if (lane == 0) {
-            const uint32_t id = idesc8(kTileCh, nt);
-            const uint32_t acc_cols = (uint32_t)p.acc_cols;
-            int s = 0, tl = 0;
-            uint32_t ph = 0, sb = base;
-            bool ok = true;
-            for (int t = first; t < n_tiles && ok; t += step, ++tl) {
-                const uint32_t buf = tl & 1;
-                if (!(ok = wait8(ctl, acc_empty + 8u * buf, ((tl >> 1) & 1) ^ 1))) break;
+        // The whole warp runs the loop and one lane is elected for the instructions:
+        // that keeps descriptors in uniform registers (with one lane inside a branch
+        // every tcgen05.mma cost ~110 cycles of issue, now ~64).
+        const uint32_t id = idesc8(kTileCh, nt);
+        const uint32_t acc_cols = (uint32_t)p.acc_cols;
+        int s = 0, tl = 0;
+        uint32_t ph = 0, sb = base;
+        bool ok = true;
+        for (int t = first; t < n_tiles && ok; t += step, ++tl) {
+            const uint32_t buf = tl & 1;
+            if (!(ok = __all_sync(0xffffffffu, wait8(ctl, acc_empty + 8u * buf, ((tl >> 1) & 1) ^ 1)))) break;
+            fence_after8();
+            const uint32_t d = tmem + buf * acc_cols;
+            uint32_t add = 0;                      // the tile's first product starts the sums
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!(ok = __all_sync(0xffffffffu, wait8(ctl, full + 8u * (uint32_t)s, ph)))) break;
                 fence_after8();
-                const uint32_t d = tmem + buf * acc_cols;
-                uint32_t add = 0;                  // the tile's first product starts the sums
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!(ok = wait8(ctl, full + 8u * (uint32_t)s, ph))) break;
-                    fence_after8();
-                    const uint64_t ad = desc8(sb), bd = desc8(sb + kWBytes);
+                const uint64_t ad = desc8(sb), bd = desc8(sb + kWBytes);
+                if (elect8()) {
                     mma_i8(d, ad, bd, id, add);
                     mma_i8(d, ad + 2, bd + 2, id, 1);
                     mma_i8(d, ad + 4, bd + 4, id, 1);
                     mma_i8(d, ad + 6, bd + 6, id, 1);
-                    add = 1;
                     commit8(empty + 8u * (uint32_t)s);
-                    sb += stage_bytes;
-                    if (++s == stages) { s = 0; ph ^= 1; sb = base; }
                 }
-                if (ok) commit8(acc_full + 8u * buf);
+                __syncwarp();
+                add = 1;
+                sb += stage_bytes;
+                if (++s == stages) { s = 0; ph ^= 1; sb = base; }
             }
+            if (ok && elect8()) commit8(acc_full + 8u * buf);
+            __syncwarp();
         }
     } else {
         const int q = warp & 3, hw = warp >> 2;    // accumulator lanes 32q .. 32q + 31
