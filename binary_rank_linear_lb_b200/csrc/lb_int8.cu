@@ -246,6 +246,16 @@ __device__ __noinline__ bool wait8_slow(volatile int* abort, uint32_t bar, uint3
         }
     }
 }
+// Whether a barrier's phase is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test8(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 // Waits for a barrier's phase; false when it gave up (bounded, about 2 s).
 __device__ __forceinline__ bool wait8(Ctl8* c, uint32_t bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait8_slow(&c->abort, bar, parity);
@@ -335,16 +345,22 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
     const uint32_t full = s32(&ctl->full[0]), empty = s32(&ctl->empty[0]);
     const uint32_t acc_full = s32(&ctl->acc_full[0]), acc_empty = s32(&ctl->acc_empty[0]);
 
-    // The loading thread sets up the stages' barriers and requests the first stages
-    // before anything else; TMEM and the other barriers follow meanwhile.
+    // The loading warp sets up the stages' barriers and requests the first stages
+    // before anything else; TMEM and the other barriers follow meanwhile.  (It and
+    // the issuing warp run their loops whole, with one lane elected for the
+    // instructions: that keeps addresses and descriptors in uniform registers.  With
+    // one lane inside a branch a tcgen05.mma took ~110 cycles to issue, now ~64.)
     int ls = 0, lkb = kb0, lt = first;             // its position: stage, K block, tile
     uint32_t lph = 1;                              // a fresh stage counts as empty
     int lc = (first / n_tok) * kTileCh, lm = (first % n_tok) * nt;
     auto load_stage = [&] {
         const uint32_t fb = full + 8u * (uint32_t)ls, sb = base + (uint32_t)ls * stage_bytes;
-        mbar_expect_tx(fb, stage_bytes);
-        tma_load_2d(sb, &wmap, fb, lkb * kKBytes, lc);
-        tma_load_2d(sb + kWBytes, &xmap, fb, lkb * kKBytes, lm);
+        if (elect8()) {
+            mbar_expect_tx(fb, stage_bytes);
+            tma_load_2d(sb, &wmap, fb, lkb * kKBytes, lc);
+            tma_load_2d(sb + kWBytes, &xmap, fb, lkb * kKBytes, lm);
+        }
+        __syncwarp();
         if (++ls == stages) { ls = 0; lph ^= 1; }
         if (++lkb == kb1) {
             lkb = kb0;
@@ -353,12 +369,13 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
             lm = (lt % n_tok) * nt;
         }
     };
-    if (warp == kLoadWarp && lane == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(full + 8u * s, 1);
-            mbar_init(empty + 8u * s, 1);
+    if (warp == kLoadWarp) {
+        if (lane < stages) {
+            mbar_init(full + 8u * (uint32_t)lane, 1);
+            mbar_init(empty + 8u * (uint32_t)lane, 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
         for (int s = 0; s < stages && lt < n_tiles; ++s) load_stage();
     }
     if (warp == kIssueWarp) {
@@ -383,17 +400,13 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
     const uint32_t tmem = ctl->tmem_base;
 
     if (warp == kLoadWarp) {
-        if (lane == 0)
-            while (lt < n_tiles && wait8(ctl, empty + 8u * (uint32_t)ls, lph)) load_stage();
+        while (lt < n_tiles && __all_sync(0xffffffffu, wait8(ctl, empty + 8u * (uint32_t)ls, lph))) load_stage();
     } else if (warp == kIssueWarp) {
-        // The whole warp runs the loop and one lane is elected for the instructions:
-        // that keeps descriptors in uniform registers (with one lane inside a branch
-        // every tcgen05.mma cost ~110 cycles of issue, now ~64).
         const uint32_t id = idesc8(kTileCh, nt);
         const uint32_t acc_cols = (uint32_t)p.acc_cols;
         int s = 0, tl = 0;
         uint32_t ph = 0, sb = base;
-        bool ok = true;
+        bool ok = true, ready = false;             // ready: the next stage is known to be full
         for (int t = first; t < n_tiles && ok; t += step, ++tl) {
             const uint32_t buf = tl & 1;
             if (!(ok = __all_sync(0xffffffffu, wait8(ctl, acc_empty + 8u * buf, ((tl >> 1) & 1) ^ 1)))) break;
@@ -401,20 +414,24 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
             const uint32_t d = tmem + buf * acc_cols;
             uint32_t add = 0;                      // the tile's first product starts the sums
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!(ok = __all_sync(0xffffffffu, wait8(ctl, full + 8u * (uint32_t)s, ph)))) break;
+                if (!__all_sync(0xffffffffu, ready) &&
+                    !(ok = __all_sync(0xffffffffu, wait8(ctl, full + 8u * (uint32_t)s, ph))))
+                    break;
                 fence_after8();
                 const uint64_t ad = desc8(sb), bd = desc8(sb + kWBytes);
+                const uint32_t done = empty + 8u * (uint32_t)s;
+                sb += stage_bytes;
+                if (++s == stages) { s = 0; ph ^= 1; sb = base; }
+                ready = mbar_test8(full + 8u * (uint32_t)s, ph);       // (asked while the MMAs issue)
                 if (elect8()) {
                     mma_i8(d, ad, bd, id, add);
                     mma_i8(d, ad + 2, bd + 2, id, 1);
                     mma_i8(d, ad + 4, bd + 4, id, 1);
                     mma_i8(d, ad + 6, bd + 6, id, 1);
-                    commit8(empty + 8u * (uint32_t)s);
+                    commit8(done);
                 }
                 __syncwarp();
                 add = 1;
-                sb += stage_bytes;
-                if (++s == stages) { s = 0; ph ^= 1; sb = base; }
             }
             if (ok && elect8()) commit8(acc_full + 8u * buf);
             __syncwarp();
