@@ -208,6 +208,7 @@ constexpr int kMaxTok = 256;                       // tokens of a tile at most
 constexpr int kKBytes = 128;                       // K per stage
 constexpr int kWBytes = kTileCh * kKBytes;         // 16 KB
 constexpr int kMaxStages8 = 12;
+constexpr int kTwoBlockTok = 160;                   // 3 stages of 2 x (16 + 20) KB
 constexpr int kPipeBytes = 216 * 1024;             // stages; then a split's partial sums
 static_assert(kTileCh * (kMaxTok + 4) * 4 <= kPipeBytes, "partial sums");
 constexpr int kMaxLgSplit = 3;                     // at most 8 CTAs share a tile
@@ -226,7 +227,8 @@ static_assert(kMmaSmem <= 232448, "shared memory");
 struct MmaPlan {
     int nt;               // tokens per tile, a multiple of 16
     int n_tok, n_ch;      // tiles along the tokens and the channels
-    int n_kb;             // K blocks
+    int kper;             // K blocks of 128 bytes a stage (1 or 2)
+    int n_kb;             // stages of a tile's K
     int lg_split;         // log2 of the CTAs that share a tile's K blocks
     int stages, stage_bytes;
     int acc_cols;         // columns of one accumulator, a multiple of 32
@@ -324,7 +326,7 @@ __device__ __forceinline__ void st_cluster8(uint32_t addr, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
 }
 
-template <int DT, bool SPLIT>
+template <int DT, bool SPLIT, int KPER>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                 const __grid_constant__ Int8Args a, const __grid_constant__ MmaPlan p) {
@@ -342,6 +344,7 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
     const int kb0 = (p.n_kb * rank) >> lg, kb1 = (p.n_kb * (rank + 1)) >> lg;
     const int stages = p.stages;
     const uint32_t stage_bytes = (uint32_t)p.stage_bytes;
+    const uint32_t x_bytes = (uint32_t)(nt * kKBytes);             // the tokens of one K block
     const uint32_t full = s32(&ctl->full[0]), empty = s32(&ctl->empty[0]);
     const uint32_t acc_full = s32(&ctl->acc_full[0]), acc_empty = s32(&ctl->acc_empty[0]);
 
@@ -357,8 +360,12 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
         const uint32_t fb = full + 8u * (uint32_t)ls, sb = base + (uint32_t)ls * stage_bytes;
         if (elect8()) {
             mbar_expect_tx(fb, stage_bytes);
-            tma_load_2d(sb, &wmap, fb, lkb * kKBytes, lc);
-            tma_load_2d(sb + kWBytes, &xmap, fb, lkb * kKBytes, lm);
+#pragma unroll
+            for (int k = 0; k < KPER; ++k) {
+                const int col = (lkb * KPER + k) * kKBytes;
+                tma_load_2d(sb + k * kWBytes, &wmap, fb, col, lc);
+                tma_load_2d(sb + KPER * kWBytes + (uint32_t)k * x_bytes, &xmap, fb, col, lm);
+            }
         }
         __syncwarp();
         if (++ls == stages) { ls = 0; lph ^= 1; }
@@ -418,16 +425,18 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
                     !(ok = __all_sync(0xffffffffu, wait8(ctl, full + 8u * (uint32_t)s, ph))))
                     break;
                 fence_after8();
-                const uint64_t ad = desc8(sb), bd = desc8(sb + kWBytes);
+                const uint64_t ad = desc8(sb), bd = desc8(sb + KPER * kWBytes);
                 const uint32_t done = empty + 8u * (uint32_t)s;
                 sb += stage_bytes;
                 if (++s == stages) { s = 0; ph ^= 1; sb = base; }
                 ready = mbar_test8(full + 8u * (uint32_t)s, ph);       // (asked while the MMAs issue)
                 if (elect8()) {
-                    mma_i8(d, ad, bd, id, add);
-                    mma_i8(d, ad + 2, bd + 2, id, 1);
-                    mma_i8(d, ad + 4, bd + 4, id, 1);
-                    mma_i8(d, ad + 6, bd + 6, id, 1);
+#pragma unroll
+                    for (int k = 0; k < KPER; ++k)
+#pragma unroll
+                        for (int kk = 0; kk < kKBytes / 32; ++kk)
+                            mma_i8(d, ad + (uint64_t)(k * (kWBytes / 16) + 2 * kk),
+                                   bd + (uint64_t)((uint32_t)k * (x_bytes / 16u) + 2u * kk), id, k + kk ? 1u : add);
                     commit8(done);
                 }
                 __syncwarp();
@@ -587,12 +596,15 @@ MmaPlan mma_plan(int64_t M, int64_t N, int64_t K, int sms) {
     p.nt = (int)(((M + p.n_tok - 1) / p.n_tok + 15) / 16 * 16);
     p.n_tok = (int)((M + p.nt - 1) / p.nt);
     p.n_ch = (int)((N + kTileCh - 1) / kTileCh);
-    p.n_kb = (int)((K + kKBytes - 1) / kKBytes);
+    // two K blocks a stage where three such stages fit: half the waits and commits
+    // (of the ~450 cycles that a stage of one block took to issue, ~190 were those)
+    p.kper = p.nt <= kTwoBlockTok ? 2 : 1;
+    p.n_kb = (int)((K + p.kper * kKBytes - 1) / (p.kper * kKBytes));
     const int64_t tiles = (int64_t)p.n_tok * p.n_ch;
     // halve the K range while the clusters fit the SMs and a part keeps 4 blocks
-    while (p.lg_split < kMaxLgSplit && (tiles << (p.lg_split + 1)) <= sms && (p.n_kb >> (p.lg_split + 1)) >= 4)
+    while (p.lg_split < kMaxLgSplit && (tiles << (p.lg_split + 1)) <= sms && ((p.n_kb * p.kper) >> (p.lg_split + 1)) >= 4)
         ++p.lg_split;
-    p.stage_bytes = kWBytes + p.nt * kKBytes;
+    p.stage_bytes = p.kper * (kWBytes + p.nt * kKBytes);
     p.stages = std::min(kPipeBytes / p.stage_bytes, kMaxStages8);
     p.acc_cols = (p.nt + 31) / 32 * 32;
     p.tmem_cols = 64;
@@ -600,7 +612,7 @@ MmaPlan mma_plan(int64_t M, int64_t N, int64_t K, int sms) {
     return p;
 }
 
-template <int DT, bool SPLIT>
+template <int DT, bool SPLIT, int KPER>
 cudaError_t launch_mma(const Int8Args& a, const MmaPlan& p, const CUtensorMap& wm, const CUtensorMap& xm,
                        int sms, cudaStream_t s) {
     const int64_t tiles = (int64_t)p.n_tok * p.n_ch;
@@ -615,10 +627,10 @@ cudaError_t launch_mma(const Int8Args& a, const MmaPlan& p, const CUtensorMap& w
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = SPLIT ? 1 : 0;
-    cudaError_t e = cudaFuncSetAttribute(int8_mma_kernel<DT, SPLIT>,
+    cudaError_t e = cudaFuncSetAttribute(int8_mma_kernel<DT, SPLIT, KPER>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
     if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&cfg, int8_mma_kernel<DT, SPLIT>, wm, xm, a, p);
+    return cudaLaunchKernelEx(&cfg, int8_mma_kernel<DT, SPLIT, KPER>, wm, xm, a, p);
 }
 
 // The tensor-core kernel reads rows through tensor maps: 16-byte pieces.
@@ -665,8 +677,11 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
             !code_map(&xm, xq, M, in, M == 1 ? (in + 15) / 16 * 16 : ldx, p.nt))
             return LB_ERR_CUDA;
         const cudaError_t e = with_dtype(y_dtype, [&](auto d) {
-            return p.lg_split > 0 ? launch_mma<d.value, true>(a, p, wm, xm, sms, s)
-                               : launch_mma<d.value, false>(a, p, wm, xm, sms, s);
+            if (p.kper == 1)
+                return p.lg_split > 0 ? launch_mma<d.value, true, 1>(a, p, wm, xm, sms, s)
+                                      : launch_mma<d.value, false, 1>(a, p, wm, xm, sms, s);
+            return p.lg_split > 0 ? launch_mma<d.value, true, 2>(a, p, wm, xm, sms, s)
+                                  : launch_mma<d.value, false, 2>(a, p, wm, xm, sms, s);
         });
         return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
     }
