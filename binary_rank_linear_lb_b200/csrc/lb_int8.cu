@@ -237,17 +237,6 @@ struct MmaPlan {
 
 __device__ __forceinline__ uint32_t s32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __noinline__ bool wait8_slow(volatile int* abort, uint32_t bar, uint32_t parity) {
-    const long long t0 = clock64();
-    while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (clock64() - t0 > kWaitLimit8) {
-            *abort = 1;
-            return false;
-        }
-    }
-}
 // Whether a barrier's phase is complete, without waiting for it.
 __device__ __forceinline__ bool mbar_test8(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -258,9 +247,19 @@ __device__ __forceinline__ bool mbar_test8(uint32_t bar, uint32_t parity) {
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// Waits for a barrier's phase; false when it gave up (bounded, about 2 s).
+// Waits for a barrier's phase; false when it gave up (bounded, about 2 s).  (Inline:
+// around a call the loops' addresses and descriptors would leave the uniform registers.)
 __device__ __forceinline__ bool wait8(Ctl8* c, uint32_t bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait8_slow(&c->abort, bar, parity);
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int*>(&c->abort)) return false;
+        if (clock64() - t0 > kWaitLimit8) {
+            *reinterpret_cast<volatile int*>(&c->abort) = 1;
+            return false;
+        }
+    }
 }
 
 // Shared-memory descriptor: K-major, 128-byte swizzle, 8-row atoms of 1024 bytes.
@@ -411,9 +410,13 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
     } else if (warp == kIssueWarp) {
         const uint32_t id = idesc8(kTileCh, nt);
         const uint32_t acc_cols = (uint32_t)p.acc_cols;
-        int s = 0, tl = 0;
-        uint32_t ph = 0, sb = base;
-        bool ok = true, ready = false;             // ready: the next stage is known to be full
+        const uint64_t ad0 = desc8(base), bd0 = desc8(base + KPER * kWBytes);
+        const uint32_t stage16 = stage_bytes / 16u, x16 = x_bytes / 16u;
+        uint64_t ad = ad0, bd = bd0;               // the current stage's descriptors
+        uint32_t ph = 0, fb = full, eb = empty;    // and barriers
+        const uint32_t fb_end = full + 8u * (uint32_t)stages;
+        int tl = 0;
+        bool ok = true, ready = false;             // ready: the current stage is known to be full
         for (int t = first; t < n_tiles && ok; t += step, ++tl) {
             const uint32_t buf = tl & 1;
             if (!(ok = __all_sync(0xffffffffu, wait8(ctl, acc_empty + 8u * buf, ((tl >> 1) & 1) ^ 1)))) break;
@@ -421,26 +424,25 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
             const uint32_t d = tmem + buf * acc_cols;
             uint32_t add = 0;                      // the tile's first product starts the sums
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!__all_sync(0xffffffffu, ready) &&
-                    !(ok = __all_sync(0xffffffffu, wait8(ctl, full + 8u * (uint32_t)s, ph))))
-                    break;
+                if (!__all_sync(0xffffffffu, ready) && !(ok = __all_sync(0xffffffffu, wait8(ctl, fb, ph)))) break;
                 fence_after8();
-                const uint64_t ad = desc8(sb), bd = desc8(sb + KPER * kWBytes);
-                const uint32_t done = empty + 8u * (uint32_t)s;
-                sb += stage_bytes;
-                if (++s == stages) { s = 0; ph ^= 1; sb = base; }
-                ready = mbar_test8(full + 8u * (uint32_t)s, ph);       // (asked while the MMAs issue)
                 if (elect8()) {
 #pragma unroll
                     for (int k = 0; k < KPER; ++k)
 #pragma unroll
                         for (int kk = 0; kk < kKBytes / 32; ++kk)
                             mma_i8(d, ad + (uint64_t)(k * (kWBytes / 16) + 2 * kk),
-                                   bd + (uint64_t)((uint32_t)k * (x_bytes / 16u) + 2u * kk), id, k + kk ? 1u : add);
-                    commit8(done);
+                                   bd + (uint64_t)((uint32_t)k * x16 + 2u * kk), id, k + kk ? 1u : add);
+                    commit8(eb);
                 }
                 __syncwarp();
                 add = 1;
+                ad += stage16;
+                bd += stage16;
+                fb += 8u;
+                eb += 8u;
+                if (fb == fb_end) { fb = full; eb = empty; ph ^= 1; ad = ad0; bd = bd0; }
+                ready = mbar_test8(fb, ph);        // (asked while the MMAs run)
             }
             if (ok && elect8()) commit8(acc_full + 8u * buf);
             __syncwarp();
