@@ -209,6 +209,8 @@ constexpr int kKBytes = 128;                       // K per stage
 constexpr int kWBytes = kTileCh * kKBytes;         // 16 KB
 constexpr int kMaxStages8 = 12;
 constexpr int kTwoBlockTok = 160;                   // 3 stages of 2 x (16 + 20) KB
+constexpr int kTwoBlockPair = 96;
+constexpr int kSingleTok = 96;                      // up to here only single CTAs
 constexpr int kPipeBytes = 216 * 1024;             // stages; then a split's partial sums
 static_assert(kTileCh * (kMaxTok + 4) * 4 <= kPipeBytes, "partial sums");
 constexpr int kMaxLgSplit = 3;                     // at most 8 CTAs share a tile
@@ -219,13 +221,15 @@ struct Ctl8 {
     uint64_t full[kMaxStages8], empty[kMaxStages8], acc_full[2], acc_empty[2];
     uint32_t tmem_base;
     int abort;
+    alignas(16) float xbuf[kDrainWarps][32];       // token scales of the columns being stored
     int lost[kMaxSplit8];                          // split: CTA r of the cluster gave up
 };
 constexpr int kMmaSmem = kPipeBytes + (int)sizeof(Ctl8) + 1024;
 static_assert(kMmaSmem <= 232448, "shared memory");
 
 struct MmaPlan {
-    int nt;               // tokens per tile, a multiple of 16
+    int pair;             // two CTAs on a tile of 256 channels (else one, 128 channels)
+    int nt;               // tokens per tile, a multiple of 16 (pairs: 32)
     int n_tok, n_ch;      // tiles along the tokens and the channels
     int kper;             // K blocks of 128 bytes a stage (1 or 2)
     int n_kb;             // stages of a tile's K
@@ -323,6 +327,47 @@ __device__ __forceinline__ void st_cluster8(uint32_t addr, int a, int b, int c, 
 }
 __device__ __forceinline__ void st_cluster8(uint32_t addr, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
+}
+
+// Waits for an accumulator and stores it, a warp a quarter of the lanes (lane =
+// channel c0 + 32 (warp & 3) + lane) and every other 32 columns (tokens m0 ..).  The
+// tokens' scales go through a shared buffer of the warp (xbuf, 32 floats) to be read
+// four at a time: a shuffle a column shared the stores' queue.
+template <int DT>
+__device__ __forceinline__ void drain_tile(Ctl8* ctl, const Int8Args& a, uint32_t bar, uint32_t parity, uint32_t tacc,
+                                           int c0, int m0, int nt, float* xbuf, int warp, int lane) {
+    using Y = Elem<DT>;
+    const int q = warp & 3, hw = warp >> 2, n = c0 + q * 32 + lane;
+    float ws = n < a.N ? __ldg(a.ws + n) : 0.0f;
+    const int cols = min(nt, a.M - m0);
+    float xl = lane < cols - 32 * hw ? __ldg(a.xs + m0 + 32 * hw + lane) : 0.0f;
+    // every lane waits; the warp goes on together (the TMEM loads are warp-wide)
+    const bool ok = __all_sync(0xffffffffu, wait8(ctl, bar, parity));
+    fence_after8();
+    if (!ok) ws = __int_as_float(0x7fc00000);      // NaN: the sums are not there
+    tacc += (uint32_t)(q * 32) << 16;
+    const int64_t ldy = a.ldy;
+    for (int j = 32 * hw; j < cols; j += 64) {
+        int v[32];
+        __syncwarp();
+        xbuf[lane] = xl;
+        if (ok) tmem_ld8(tacc + (uint32_t)j, v);
+        xl = lane < cols - (j + 64) ? __ldg(a.xs + m0 + j + 64 + lane) : 0.0f;
+        __syncwarp();
+        typename Y::T* y = static_cast<typename Y::T*>(a.y) + (int64_t)(m0 + j) * ldy + n;
+        const bool whole = j + 32 <= cols && c0 + kTileCh <= a.N;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 x4 = *reinterpret_cast<const float4*>(xbuf + i);
+            const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const typename Y::T o = Y::put((float)v[i + k] * xs[k] * ws);
+                if (whole || (j + i + k < cols && n < a.N)) *y = o;
+                y += ldy;
+            }
+        }
+    }
 }
 
 template <int DT, bool SPLIT, int KPER>
@@ -447,65 +492,38 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
             if (ok && elect8()) commit8(acc_full + 8u * buf);
             __syncwarp();
         }
+    } else if constexpr (SPLIT) {
+        if (first < n_tiles) {                     // (a split call has one tile per cluster)
+            // Once every CTA of the cluster has its sums (its stages are free then),
+            // each gives the others their channels' partial sums: [source][channel]
+            // [token], a channel's row padded to an odd number of 16-byte pieces.
+            const int q = warp & 3, hw = warp >> 2;
+            const bool ok = __all_sync(0xffffffffu, wait8(ctl, acc_full, 0));
+            fence_after8();
+            cluster_arrive8();
+            cluster_wait8();
+            const uint32_t per = (uint32_t)kTileCh >> lg;              // channels a CTA folds
+            const uint32_t ch = (uint32_t)(q * 32 + lane), pitch = 4u * (uint32_t)(nt + 4);
+            const uint32_t dst = peer_addr8(base + ((uint32_t)rank * per + (ch & (per - 1))) * pitch, ch >> (7 - lg));
+            for (int j = 32 * hw; j < nt; j += 64) {
+                int v[32];
+                __syncwarp();
+                if (ok) tmem_ld8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)j, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    if (j + i < nt) st_cluster8(dst + 4u * (uint32_t)(j + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+            if (!ok && lane < (1 << lg)) st_cluster8(peer_addr8(s32(&ctl->lost[rank]), (uint32_t)lane), 1);
+        }
     } else {
-        const int q = warp & 3, hw = warp >> 2;    // accumulator lanes 32q .. 32q + 31
         int tl = 0;
         for (int t = first; t < n_tiles; t += step, ++tl) {
-            const int c0 = (t / n_tok) * kTileCh, m0 = (t % n_tok) * nt;
             const uint32_t buf = tl & 1;
-            const int n = c0 + q * 32 + lane;
-            float ws = n < a.N ? __ldg(a.ws + n) : 0.0f;
-            const int cols = min(nt, a.M - m0);
-            float xl = lane < cols - 32 * hw ? __ldg(a.xs + m0 + 32 * hw + lane) : 0.0f;
-            // every lane waits; the warp goes on together (the TMEM loads are warp-wide)
-            const bool ok = __all_sync(0xffffffffu, wait8(ctl, acc_full + 8u * buf, (tl >> 1) & 1));
-            fence_after8();
-            const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + buf * (uint32_t)p.acc_cols;
-            if constexpr (SPLIT) {
-                // Once every CTA of the cluster has its sums (its stages are free then),
-                // each gives the others their channels' partial sums: [source][channel]
-                // [token], a channel's row padded to an odd number of 16-byte pieces.
-                cluster_arrive8();
-                cluster_wait8();
-                const uint32_t per = (uint32_t)kTileCh >> lg;          // channels a CTA folds
-                const uint32_t ch = (uint32_t)(q * 32 + lane), pitch = 4u * (uint32_t)(nt + 4);
-                const uint32_t dst = peer_addr8(base + ((uint32_t)rank * per + (ch & (per - 1))) * pitch, ch >> (7 - lg));
-                for (int j = 32 * hw; j < nt; j += 64) {
-                    int v[32];
-                    __syncwarp();
-                    if (ok) tmem_ld8(tacc + (uint32_t)j, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        if (j + i < nt) st_cluster8(dst + 4u * (uint32_t)(j + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
-                }
-                if (!ok && lane < (1 << lg)) st_cluster8(peer_addr8(s32(&ctl->lost[rank]), (uint32_t)lane), 1);
-                break;                             // (a split call has one tile per cluster)
-            } else {
-                if (!ok) ws = __int_as_float(0x7fc00000);              // NaN: the sums are not there
-                for (int j = 32 * hw; j < cols; j += 64) {
-                    int v[32];
-                    __syncwarp();
-                    if (ok) tmem_ld8(tacc + (uint32_t)j, v);
-                    const float xn = lane < cols - (j + 64) ? __ldg(a.xs + m0 + j + 64 + lane) : 0.0f;
-                    typename Y::T* y = static_cast<typename Y::T*>(a.y) + (int64_t)(m0 + j) * a.ldy + n;
-                    const int64_t ldy = a.ldy;
-                    if (j + 32 <= cols && c0 + kTileCh <= a.N) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            y[i * ldy] = Y::put((float)v[i] * __shfl_sync(0xffffffffu, xl, i) * ws);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float xs = __shfl_sync(0xffffffffu, xl, i);
-                            if (j + i < cols && n < a.N) y[i * ldy] = Y::put((float)v[i] * xs * ws);
-                        }
-                    }
-                    xl = xn;
-                }
-                fence_before8();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
-            }
+            drain_tile<DT>(ctl, a, acc_full + 8u * buf, (tl >> 1) & 1, tmem + buf * (uint32_t)p.acc_cols,
+                           (t / n_tok) * kTileCh, (t % n_tok) * nt, nt, ctl->xbuf[warp], warp, lane);
+            fence_before8();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
         }
     }
     if constexpr (SPLIT) {
@@ -560,6 +578,173 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
     }
 }
 
+// The same with two CTAs on a tile of 256 channels (tcgen05 cta_group::2): each
+// loads its own 128 channels and half of the tokens, the first one issues the MMAs
+// for both, and each drains its own channels.  A CTA then brings in 32 KB for a
+// K block of 256 tokens instead of 48 KB.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];"
+        :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs when the MMAs so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        :: "r"(bar), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void arrive_peer8(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
+template <int DT, int KPER>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+int8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                 const __grid_constant__ Int8Args a, const __grid_constant__ MmaPlan p) {
+    using Y = Elem<DT>;
+    extern __shared__ __align__(1024) unsigned char dsm[];
+    const uint32_t raw = s32(dsm);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    Ctl8* ctl = reinterpret_cast<Ctl8*>(dsm + (base - raw) + kPipeBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)(blockIdx.x & 1u);
+    const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
+    const int n_tok = p.n_tok, n_tiles = n_tok * p.n_ch, nt = p.nt, n_kb = p.n_kb;
+    const int stages = p.stages;
+    const uint32_t stage_bytes = (uint32_t)p.stage_bytes, x_bytes = (uint32_t)(nt / 2 * kKBytes);
+    const uint32_t full = s32(&ctl->full[0]), empty = s32(&ctl->empty[0]);
+    const uint32_t acc_full = s32(&ctl->acc_full[0]), acc_empty = s32(&ctl->acc_empty[0]);
+
+    if (warp == kLoadWarp) {
+        if (lane < stages) {
+            mbar_init(full + 8u * (uint32_t)lane, 1);
+            mbar_init(empty + 8u * (uint32_t)lane, 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kIssueWarp) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(acc_full + 8u * i, 1);
+                mbar_init(acc_empty + 8u * i, 2 * kDrainWarps);        // (the first CTA's; both drain)
+            }
+            ctl->abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(s32(&ctl->tmem_base)), "r"(p.tmem_cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    __syncwarp();
+    fence_before8();
+    __syncthreads();
+    cluster_arrive8();
+    cluster_wait8();                               // both CTAs' barriers are set up
+    fence_after8();
+    const uint32_t tmem = ctl->tmem_base;
+
+    if (warp == kLoadWarp) {
+        // both CTAs' copies count on the first CTA's barrier
+        const uint32_t full0 = peer_addr8(full, 0);
+        int s = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int t = first; t < n_tiles && ok; t += step) {
+            const int c0 = (t / n_tok) * 2 * kTileCh + rank * kTileCh, m0 = (t % n_tok) * nt + rank * (nt / 2);
+            for (int kb = 0; kb < n_kb; ++kb) {
+                if (!(ok = __all_sync(0xffffffffu, wait8(ctl, empty + 8u * (uint32_t)s, ph)))) break;
+                const uint32_t sb = base + (uint32_t)s * stage_bytes, fb = full0 + 8u * (uint32_t)s;
+                if (elect8()) {
+                    if (rank == 0) mbar_expect_tx(full + 8u * (uint32_t)s, 2u * stage_bytes);
+#pragma unroll
+                    for (int k = 0; k < KPER; ++k) {
+                        const int col = (kb * KPER + k) * kKBytes;
+                        tma_load_pair(sb + k * kWBytes, &wmap, fb, col, c0);
+                        tma_load_pair(sb + KPER * kWBytes + (uint32_t)k * x_bytes, &xmap, fb, col, m0);
+                    }
+                }
+                __syncwarp();
+                if (++s == stages) { s = 0; ph ^= 1; }
+            }
+        }
+    } else if (warp == kIssueWarp) {
+        if (rank == 0) {
+            const uint32_t id = idesc8(2 * kTileCh, nt);
+            const uint32_t acc_cols = (uint32_t)p.acc_cols;
+            const uint64_t ad0 = desc8(base), bd0 = desc8(base + KPER * kWBytes);
+            const uint32_t stage16 = stage_bytes / 16u, x16 = x_bytes / 16u;
+            uint64_t ad = ad0, bd = bd0;
+            uint32_t ph = 0, fb = full, eb = empty;
+            const uint32_t fb_end = full + 8u * (uint32_t)stages;
+            int tl = 0;
+            bool ok = true, ready = false;
+            for (int t = first; t < n_tiles && ok; t += step, ++tl) {
+                const uint32_t buf = tl & 1;
+                if (!(ok = __all_sync(0xffffffffu, wait8(ctl, acc_empty + 8u * buf, ((tl >> 1) & 1) ^ 1)))) break;
+                fence_after8();
+                const uint32_t d = tmem + buf * acc_cols;
+                uint32_t add = 0;
+                for (int kb = 0; kb < n_kb; ++kb) {
+                    if (!__all_sync(0xffffffffu, ready) && !(ok = __all_sync(0xffffffffu, wait8(ctl, fb, ph)))) break;
+                    fence_after8();
+                    if (elect8()) {
+#pragma unroll
+                        for (int k = 0; k < KPER; ++k)
+#pragma unroll
+                            for (int kk = 0; kk < kKBytes / 32; ++kk)
+                                mma_i8_pair(d, ad + (uint64_t)(k * (kWBytes / 16) + 2 * kk),
+                                            bd + (uint64_t)((uint32_t)k * x16 + 2u * kk), id, k + kk ? 1u : add);
+                        commit_pair(eb);
+                    }
+                    __syncwarp();
+                    add = 1;
+                    ad += stage16;
+                    bd += stage16;
+                    fb += 8u;
+                    eb += 8u;
+                    if (fb == fb_end) { fb = full; eb = empty; ph ^= 1; ad = ad0; bd = bd0; }
+                    ready = mbar_test8(fb, ph);
+                }
+                if (ok && elect8()) commit_pair(acc_full + 8u * buf);
+                __syncwarp();
+            }
+        }
+    } else {
+        const uint32_t acc_empty0 = peer_addr8(acc_empty, 0);
+        int tl = 0;
+        for (int t = first; t < n_tiles; t += step, ++tl) {
+            const uint32_t buf = tl & 1;
+            drain_tile<DT>(ctl, a, acc_full + 8u * buf, (tl >> 1) & 1, tmem + buf * (uint32_t)p.acc_cols,
+                           (t / n_tok) * 2 * kTileCh + rank * kTileCh, (t % n_tok) * nt, nt, ctl->xbuf[warp], warp, lane);
+            fence_before8();
+            __syncwarp();
+            if (lane == 0) arrive_peer8(acc_empty0 + 8u * buf);
+        }
+    }
+    __syncthreads();
+    if (ctl->abort && threadIdx.x == 0) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000LL) { }
+    }
+    __syncthreads();
+    cluster_arrive8();
+    cluster_wait8();                               // neither CTA leaves while the other may signal it
+    if (warp == kIssueWarp) {
+        fence_after8();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+                     :: "r"(tmem), "r"(p.tmem_cols) : "memory");
+    }
+}
+
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -591,22 +776,50 @@ bool code_map(CUtensorMap* map, const int8_t* ptr, int64_t rows, int64_t k, int6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tiles, K split and stages of a call on `sms` SMs.
+// The plan of a call on `sms` SMs: single CTAs or pairs, tokens per tile, K split.
+// Each candidate is given its time in cycles and the shortest is taken.  A K block
+// (128 bytes of K) of a tile costs what its operands take from L2 at 64 bytes a
+// clock and SM, which is what every shape with several rounds measured (4096 ->
+// 11008 at 1000 tokens, tiles of 208 tokens by single CTAs: 672 cycles a block by
+// this rule, 38 us; pairs with 224 tokens: 480 cycles, 37 us; with 192, a fourth
+// round, 40 us), and at least ~300 to issue.  A pair's K block of 256 tokens takes
+// 512 cycles to bring in and 512 to multiply.  Then come the last tile's stores,
+// ~25 cycles a token, or a split's exchange, ~3000 + 55 a token.
 MmaPlan mma_plan(int64_t M, int64_t N, int64_t K, int sms) {
-    MmaPlan p = {};
-    p.n_tok = (int)((M + kMaxTok - 1) / kMaxTok);
-    p.nt = (int)(((M + p.n_tok - 1) / p.n_tok + 15) / 16 * 16);
-    p.n_tok = (int)((M + p.nt - 1) / p.nt);
-    p.n_ch = (int)((N + kTileCh - 1) / kTileCh);
-    // two K blocks a stage where three such stages fit: half the waits and commits
-    // (of the ~450 cycles that a stage of one block took to issue, ~190 were those)
-    p.kper = p.nt <= kTwoBlockTok ? 2 : 1;
+    MmaPlan best = {};
+    int64_t best_cost = -1;
+    const int64_t blocks = (K + kKBytes - 1) / kKBytes;
+    const int64_t least = (M + kMaxTok - 1) / kMaxTok;             // token tiles at least
+    for (int pair = 0; pair <= (M > kSingleTok ? 1 : 0); ++pair) {
+        const int grain = pair ? 32 : 16, ch = pair ? 2 * kTileCh : kTileCh;
+        const int64_t n_ch = (N + ch - 1) / ch, ctas = pair ? sms / 2 : sms;
+        for (int64_t tok = least; tok < least + 8 && (tok - 1) * grain < M; ++tok) {
+            const int nt = (int)((M + tok - 1) / tok + grain - 1) / grain * grain;
+            const int64_t n_tok = (M + nt - 1) / nt, tiles = n_tok * n_ch;
+            const int64_t block = std::max<int64_t>(300, pair ? 256 + nt : 2 * (kTileCh + nt));
+            for (int lg = 0; lg <= (pair ? 0 : kMaxLgSplit); ++lg) {
+                // (a split has a cluster per tile, all at once, and at least 4 blocks a part)
+                if (lg > 0 && ((tiles << lg) > sms || (blocks >> lg) < 4)) break;
+                const int64_t rounds = lg > 0 ? 1 : (tiles + ctas - 1) / ctas;
+                const int64_t cost = rounds * ((blocks + (1 << lg) - 1) >> lg) * block +
+                                     (lg > 0 ? 3000 + 55 * nt : 25 * nt);
+                if (best_cost >= 0 && cost >= best_cost) continue;
+                best_cost = cost;
+                best.pair = pair;
+                best.nt = nt;
+                best.n_tok = (int)n_tok;
+                best.n_ch = (int)n_ch;
+                best.lg_split = lg;
+            }
+        }
+    }
+    MmaPlan p = best;
+    const int x_rows = p.pair ? p.nt / 2 : p.nt;                    // tokens that one CTA loads
+    // Two K blocks a stage halve the waits and commits: worth it while the tiles are
+    // small (pairs of 64 tokens 12.7 -> 12.5 us, of 192 tokens 23.6 -> 26.2 us).
+    p.kper = p.nt <= (p.pair ? kTwoBlockPair : kTwoBlockTok) ? 2 : 1;
     p.n_kb = (int)((K + p.kper * kKBytes - 1) / (p.kper * kKBytes));
-    const int64_t tiles = (int64_t)p.n_tok * p.n_ch;
-    // halve the K range while the clusters fit the SMs and a part keeps 4 blocks
-    while (p.lg_split < kMaxLgSplit && (tiles << (p.lg_split + 1)) <= sms && ((p.n_kb * p.kper) >> (p.lg_split + 1)) >= 4)
-        ++p.lg_split;
-    p.stage_bytes = p.kper * (kWBytes + p.nt * kKBytes);
+    p.stage_bytes = p.kper * (kWBytes + x_rows * kKBytes);
     p.stages = std::min(kPipeBytes / p.stage_bytes, kMaxStages8);
     p.acc_cols = (p.nt + 31) / 32 * 32;
     p.tmem_cols = 64;
@@ -633,6 +846,26 @@ cudaError_t launch_mma(const Int8Args& a, const MmaPlan& p, const CUtensorMap& w
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, int8_mma_kernel<DT, SPLIT, KPER>, wm, xm, a, p);
+}
+
+template <int DT, int KPER>
+cudaError_t launch_pair(const Int8Args& a, const MmaPlan& p, const CUtensorMap& wm, const CUtensorMap& xm,
+                        int sms, cudaStream_t s) {
+    const int64_t tiles = (int64_t)p.n_tok * p.n_ch;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, sms / 2)));
+    cfg.blockDim = dim3(kMmaThreads);
+    cfg.dynamicSmemBytes = kMmaSmem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaFuncSetAttribute(int8_pair_kernel<DT, KPER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, int8_pair_kernel<DT, KPER>, wm, xm, a, p);
 }
 
 // The tensor-core kernel reads rows through tensor maps: 16-byte pieces.
@@ -668,7 +901,7 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return LB_ERR_CUDA;
-        if (M <= kFewTok && (M <= 2 || in * out < (1 << 25)) && !getenv("NOFEW")) {
+        if (M <= kFewTok && (M <= 2 || in * out < (1 << 25))) {
             const cudaError_t e = with_dtype(y_dtype, [&](auto d) { return launch_few<d.value>(a, sms, s); });
             return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
         }
@@ -676,9 +909,12 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
         CUtensorMap wm, xm;
         // (the pitch of a single row is never used; the map wants a multiple of 16)
         if (!code_map(&wm, wq, out, in, out == 1 ? (in + 15) / 16 * 16 : ldw, kTileCh) ||
-            !code_map(&xm, xq, M, in, M == 1 ? (in + 15) / 16 * 16 : ldx, p.nt))
+            !code_map(&xm, xq, M, in, M == 1 ? (in + 15) / 16 * 16 : ldx,
+                      p.pair ? p.nt / 2 : p.nt))
             return LB_ERR_CUDA;
         const cudaError_t e = with_dtype(y_dtype, [&](auto d) {
+            if (p.pair && p.kper == 1) return launch_pair<d.value, 1>(a, p, wm, xm, sms, s);
+            if (p.pair) return launch_pair<d.value, 2>(a, p, wm, xm, sms, s);
             if (p.kper == 1)
                 return p.lg_split > 0 ? launch_mma<d.value, true, 1>(a, p, wm, xm, sms, s)
                                       : launch_mma<d.value, false, 1>(a, p, wm, xm, sms, s);
