@@ -2,6 +2,9 @@
 // element types, pair arithmetic, argument helpers.
 #pragma once
 
+#include <atomic>
+#include <type_traits>
+
 #include "lb_internal.cuh"
 
 namespace lb {
@@ -110,13 +113,23 @@ inline bool dtype_ok(int t) { return t == LB_F16 || t == LB_BF16 || t == LB_F32;
 inline size_t dtype_size(int t) { return t == LB_F32 ? 4 : 2; }
 inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// LB_OK when the current device is an sm_100 part.
-inline lb_status dense_device_ok() {
-    int dev = 0, major = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-        return LB_ERR_CUDA;
-    return major == 10 ? LB_OK : LB_ERR_UNSUPPORTED;
+// LB_OK when the current device is an sm_100 part; its SM count.  (Asked once per
+// device: two runtime calls are a tenth of a small call's time on the host.)
+inline lb_status dense_device(int& sms) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];       // 0: not asked yet, -1: another part, else its SMs
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return LB_ERR_CUDA;
+    sms = known[dev].load(std::memory_order_relaxed);
+    if (sms == 0) {
+        int major = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return LB_ERR_CUDA;
+        if (major != 10) sms = -1;
+        known[dev].store(sms, std::memory_order_relaxed);
+    }
+    return sms > 0 ? LB_OK : LB_ERR_UNSUPPORTED;
 }
 
 // Calls f with the lb_dtype as a compile-time constant.

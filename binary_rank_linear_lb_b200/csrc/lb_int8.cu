@@ -892,15 +892,12 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
         return LB_ERR_INVALID_ARG;
     if (!is_aligned(xs, 4) || !is_aligned(ws, 4) || !is_aligned(y, dtype_size(y_dtype)))
         return LB_ERR_ALIGNMENT;
-    const lb_status st = dense_device_ok();
+    int sms = 0;
+    const lb_status st = dense_device(sms);
     if (st != LB_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const Int8Args a = {xq, wq, xs, ws, y, ldx, ldw, ldy, (int)M, (int)out, (int)in};
     if (mma_ok(a)) {
-        int dev = 0, sms = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return LB_ERR_CUDA;
         if (M <= kFewTok && (M <= 2 || in * out < (1 << 25))) {
             const cudaError_t e = with_dtype(y_dtype, [&](auto d) { return launch_few<d.value>(a, sms, s); });
             return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;

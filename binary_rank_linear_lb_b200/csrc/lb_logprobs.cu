@@ -534,12 +534,9 @@ extern "C" lb_status lb_token_logprobs(const void* logits, lb_dtype dtype, int64
     if (!is_aligned(logits, dtype_size(dtype)) || !is_aligned(tokens, 8) || !is_aligned(logprob, 4) ||
         !is_aligned(entropy, 4) || (top > 0 && (!is_aligned(top_id, 8) || !is_aligned(top_logprob, 4))))
         return LB_ERR_ALIGNMENT;
-    const lb_status st = dense_device_ok();
+    int sms = 0;
+    const lb_status st = dense_device(sms);
     if (st != LB_OK) return st;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return LB_ERR_CUDA;
     const LogprobArgs a = {logits, tokens, logprob, entropy, top_id, top_logprob, ld, (int)vocab, top};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e =

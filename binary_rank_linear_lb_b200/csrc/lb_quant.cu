@@ -414,7 +414,8 @@ void launch_rows(const QuantArgs& a, cudaStream_t s) {
 }
 
 lb_status quant_call(QuantArgs a, int dt, cudaStream_t s) {
-    const lb_status st = dense_device_ok();
+    int sms = 0;
+    const lb_status st = dense_device(sms);
     if (st != LB_OK) return st;
     const int64_t per16 = 16 / (int64_t)dtype_size(dt);        // elements in 16 bytes
     const bool vec = is_aligned(a.x, 16) && is_aligned(a.residual, 16) && is_aligned(a.sum, 16) &&
