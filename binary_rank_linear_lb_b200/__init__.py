@@ -361,8 +361,19 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 _empty = torch.empty_strided
 
 
-def _on(stream, tensors, call):
-    """call(stream handle), with the tensors' GPU as the current one.
+def _here(stream, dev: int, *tensors) -> Optional[int]:
+    """The handle to launch on when the call needs no other context than the present one
+    (no stream given, everything on the current GPU); None otherwise."""
+    if stream is not None or dev < 0 or dev != _current_device():
+        return None
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            return None
+    return _raw_stream(dev)
+
+
+def _elsewhere(stream, tensors, call):
+    """call() with the tensors' GPU as the current one and `stream` as its current stream.
 
     Checks that the tensors share one GPU.  With a stream other than the current one, what
     the call allocates belongs to that stream, and the given tensors are marked as in use
@@ -373,31 +384,31 @@ def _on(stream, tensors, call):
         if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError(f"all tensors must be on one CUDA device, got {t.device} and "
                              f"{tensors[0].device}")
-    if stream is None and dev == _current_device():
-        return call(_raw_stream(dev))
     with torch.cuda.device(dev):
         if stream is None:
-            return call(_raw_stream(dev))
+            return call()
         s = stream if hasattr(stream, "cuda_stream") else \
             torch.cuda.ExternalStream(int(stream), device=dev)
         if s.device.index != dev:
             raise ValueError(f"stream on {s.device}, tensors on {tensors[0].device}")
-        if s.cuda_stream == _raw_stream(dev):
-            return call(s.cuda_stream)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
+        if s.cuda_stream != _raw_stream(dev):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
         with torch.cuda.stream(s):
-            return call(s.cuda_stream)
+            return call()
 
 
 def _rows(t: torch.Tensor, what: str) -> Tuple[int, int, int]:
     """(rows, columns, row pitch) of a matrix whose rows are contiguous."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{what} must be a matrix with unit stride along its columns")
-    rows, cols = shape
-    return rows, cols, stride[0] if rows > 1 else max(cols, stride[0])
+    if t.dim() == 2:
+        rows, cols = t.shape
+        if t.is_contiguous():
+            return rows, cols, cols
+        ld, unit = t.stride()
+        if unit == 1 or cols == 1:
+            return rows, cols, ld if rows > 1 else cols
+    raise ValueError(f"{what} must be a matrix with unit stride along its columns")
 
 
 def _dtype(t: torch.dtype, what: str) -> int:
@@ -408,30 +419,25 @@ def _dtype(t: torch.dtype, what: str) -> int:
 
 
 def _vector(t: torch.Tensor, n: int, dtype: Optional[torch.dtype], what: str) -> None:
-    if t.shape != (n,) or (n > 1 and t.stride() != (1,)) or (dtype is not None and t.dtype != dtype):
+    if t.shape != (n,) or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{what} must be a contiguous vector of {n}"
                          + (f" {dtype}" if dtype is not None else "") + " elements")
 
 
-def _check_codes(q, scale, rows: int, cols: int) -> None:
-    if q is not None:
-        if q.dtype != torch.int8 or tuple(q.shape) != (rows, cols):
-            raise ValueError(f"q must be an int8 matrix of {rows} x {cols}")
-        _rows(q, "q")
-    if scale is not None:
-        _vector(scale, rows, torch.float32, "scale")
-
-
-def _new_codes(q, scale, rows: int, cols: int, dev):
-    """(q, its pitch, scale), those not given allocated; a new q has a pitch of whole
-    16-byte pieces, which linear_int8's fast kernels read."""
+def _codes(q, scale, rows: int, cols: int, dev):
+    """(q, its pitch, scale), checked, or allocated where not given; a new q has a pitch of
+    whole 16-byte pieces, which linear_int8's fast kernels read."""
     if q is None:
         ldq = (cols + 15) // 16 * 16
         q = _empty((rows, cols), (ldq, 1), dtype=torch.int8, device=dev)
     else:
+        if q.dtype != torch.int8 or q.shape != (rows, cols):
+            raise ValueError(f"q must be an int8 matrix of {rows} x {cols}")
         ldq = _rows(q, "q")[2]
     if scale is None:
         scale = _empty((rows,), (1,), dtype=torch.float32, device=dev)
+    else:
+        _vector(scale, rows, torch.float32, "scale")
     return q, ldq, scale
 
 
@@ -443,18 +449,15 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     Used for head weights (a scale per output channel) and for activations (a scale per
     token).  A new q is a view whose pitch is a multiple of 16 bytes.
     """
+    st = _here(stream, x.get_device(), q, scale)
+    if st is None:
+        return _elsewhere(stream, (x, q, scale), lambda: quantize_rows(x, q, scale))
     rows, cols, ldx = _rows(x, "x")
     dt = _dtype(x.dtype, "x")
-    if q is not None or scale is not None:
-        _check_codes(q, scale, rows, cols)
-
-    def call(st):
-        oq, ldq, osc = _new_codes(q, scale, rows, cols, x.device)
-        _check(lib().lb_quantize_rows(x.data_ptr(), dt, rows, cols, ldx, oq.data_ptr(), ldq,
-                                      osc.data_ptr(), st), "lb_quantize_rows")
-        return oq, osc
-
-    return _on(stream, (x, q, scale), call)
+    q, ldq, scale = _codes(q, scale, rows, cols, x.device)
+    _check(lib().lb_quantize_rows(x.data_ptr(), dt, rows, cols, ldx, q.data_ptr(), ldq,
+                                  scale.data_ptr(), st), "lb_quantize_rows")
+    return q, scale
 
 
 def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -467,6 +470,10 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
 
     ``sum_out`` receives s; it may be ``residual`` or ``x`` itself.
     """
+    st = _here(stream, x.get_device(), weight, residual, sum_out, q, scale)
+    if st is None:
+        return _elsewhere(stream, (x, weight, residual, sum_out, q, scale),
+                          lambda: rmsnorm_quantize(x, weight, residual, eps, sum_out, q, scale))
     rows, cols, ldx = _rows(x, "x")
     dt = _dtype(x.dtype, "x")
     wdt, ldr, lds = LB_F32, 0, 0
@@ -477,27 +484,20 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         ldr = _rows(residual, "residual")[2]
         if residual.dtype != x.dtype or residual.shape != x.shape:
             raise ValueError("residual must have x's shape and dtype")
-    if sum_out is not None:
-        if residual is None:
-            raise ValueError("sum_out needs a residual")
-        lds = _rows(sum_out, "sum_out")[2]
-        if sum_out.dtype != x.dtype or sum_out.shape != x.shape:
-            raise ValueError("sum_out must have x's shape and dtype")
-    if q is not None or scale is not None:
-        _check_codes(q, scale, rows, cols)
-
-    def call(st):
-        total, ld = sum_out, lds
-        oq, ldq, osc = _new_codes(q, scale, rows, cols, x.device)
-        if residual is not None and total is None:
-            total, ld = _empty((rows, cols), (cols, 1), dtype=x.dtype,
-                                            device=x.device), cols
-        _check(lib().lb_rmsnorm_quantize(
-            x.data_ptr(), dt, rows, cols, ldx, _ptr(residual), ldr, _ptr(total), ld, _ptr(weight),
-            wdt, eps, oq.data_ptr(), ldq, osc.data_ptr(), st), "lb_rmsnorm_quantize")
-        return oq, osc, total
-
-    return _on(stream, (x, weight, residual, sum_out, q, scale), call)
+        if sum_out is None:
+            lds = cols
+            sum_out = _empty((rows, cols), (cols, 1), dtype=x.dtype, device=x.device)
+        else:
+            lds = _rows(sum_out, "sum_out")[2]
+            if sum_out.dtype != x.dtype or sum_out.shape != x.shape:
+                raise ValueError("sum_out must have x's shape and dtype")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    q, ldq, scale = _codes(q, scale, rows, cols, x.device)
+    _check(lib().lb_rmsnorm_quantize(
+        x.data_ptr(), dt, rows, cols, ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight),
+        wdt, eps, q.data_ptr(), ldq, scale.data_ptr(), st), "lb_rmsnorm_quantize")
+    return q, scale, sum_out
 
 
 def linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
@@ -508,29 +508,26 @@ def linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.
     ``xq`` (M x in) and ``wq`` (out x in) are int8 codes with fp32 scales per row, as
     quantize_rows and rmsnorm_quantize give them; ``dtype`` is that of a new y.
     """
+    st = _here(stream, xq.get_device(), xs, wq, ws, y)
+    if st is None:
+        return _elsewhere(stream, (xq, xs, wq, ws, y),
+                          lambda: linear_int8(xq, xs, wq, ws, y, dtype))
     M, k, ldx = _rows(xq, "xq")
     n, kw, ldw = _rows(wq, "wq")
     if xq.dtype != torch.int8 or wq.dtype != torch.int8 or k != kw:
         raise ValueError("xq and wq must be int8 matrices with the same number of columns")
     _vector(xs, M, torch.float32, "xs")
     _vector(ws, n, torch.float32, "ws")
-    ldy = n
-    if y is not None:
-        dtype = y.dtype
-        if tuple(y.shape) != (M, n):
+    if y is None:
+        dt = _dtype(dtype, "y")
+        y, ldy = _empty((M, n), (n, 1), dtype=dtype, device=xq.device), n
+    else:
+        if y.shape != (M, n):
             raise ValueError(f"y must be {M} x {n}")
-        ldy = _rows(y, "y")[2]
-    dt = _dtype(dtype, "y")
-
-    def call(st):
-        out = y if y is not None else _empty((M, n), (n, 1), dtype=dtype,
-                                                          device=xq.device)
-        _check(lib().lb_linear_int8(xq.data_ptr(), ldx, xs.data_ptr(), M, wq.data_ptr(), ldw,
-                                    ws.data_ptr(), k, n, out.data_ptr(), dt, ldy, st),
-               "lb_linear_int8")
-        return out
-
-    return _on(stream, (xq, xs, wq, ws, y), call)
+        dt, ldy = _dtype(y.dtype, "y"), _rows(y, "y")[2]
+    _check(lib().lb_linear_int8(xq.data_ptr(), ldx, xs.data_ptr(), M, wq.data_ptr(), ldw,
+                                ws.data_ptr(), k, n, y.data_ptr(), dt, ldy, st), "lb_linear_int8")
+    return y
 
 
 class TokenLogprobs(NamedTuple):
@@ -547,29 +544,27 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     """lb_token_logprobs: log probabilities of ``tokens`` (int64, one per row; negative:
     none), entropy and the ``top`` (0 .. 32) most likely alternatives of logits
     (rows x vocab; -inf masks a token)."""
+    st = _here(stream, logits.get_device(), tokens)
+    if st is None:
+        return _elsewhere(stream, (logits, tokens), lambda: token_logprobs(logits, tokens, top))
     rows, vocab, ld = _rows(logits, "logits")
     dt = _dtype(logits.dtype, "logits")
-    if tokens is not None:
-        _vector(tokens, rows, torch.int64, "tokens")
     top = int(top)
     if not 0 <= top <= min(32, max(vocab, 1)):
         raise ValueError(f"top must be 0 .. {min(32, vocab)}")
-
-    def call(st):
-        dev = logits.device
-        logprob = top_id = top_lp = None
-        if tokens is not None:
-            logprob = _empty((rows,), (1,), dtype=torch.float32, device=dev)
-        entropy = _empty((rows,), (1,), dtype=torch.float32, device=dev)
-        if top:
-            top_id = _empty((rows, top), (top, 1), dtype=torch.int64, device=dev)
-            top_lp = _empty((rows, top), (top, 1), dtype=torch.float32, device=dev)
-        _check(lib().lb_token_logprobs(logits.data_ptr(), dt, rows, vocab, ld, _ptr(tokens),
-                                       _ptr(logprob), entropy.data_ptr(), top, _ptr(top_id),
-                                       _ptr(top_lp), st), "lb_token_logprobs")
-        return TokenLogprobs(logprob, entropy, top_id, top_lp)
-
-    return _on(stream, (logits, tokens), call)
+    dev = logits.device
+    logprob = top_id = top_lp = None
+    if tokens is not None:
+        _vector(tokens, rows, torch.int64, "tokens")
+        logprob = _empty((rows,), (1,), dtype=torch.float32, device=dev)
+    entropy = _empty((rows,), (1,), dtype=torch.float32, device=dev)
+    if top:
+        top_id = _empty((rows, top), (top, 1), dtype=torch.int64, device=dev)
+        top_lp = _empty((rows, top), (top, 1), dtype=torch.float32, device=dev)
+    _check(lib().lb_token_logprobs(logits.data_ptr(), dt, rows, vocab, ld, _ptr(tokens),
+                                   _ptr(logprob), entropy.data_ptr(), top, _ptr(top_id),
+                                   _ptr(top_lp), st), "lb_token_logprobs")
+    return TokenLogprobs(logprob, entropy, top_id, top_lp)
 
 
 class Head:

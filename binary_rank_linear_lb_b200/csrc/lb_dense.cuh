@@ -132,6 +132,35 @@ inline lb_status dense_device(int& sms) {
     return sms > 0 ? LB_OK : LB_ERR_UNSUPPORTED;
 }
 
+// Programmatic dependent launch.  The kernels of the dense path follow one another
+// on a stream; each lets the next one start while it still runs (grid_trigger),
+// and touches global memory only after everything before it has completed and is
+// visible (every thread calls grid_wait before its first access), so only launch
+// latency and set-up overlap.  333 x 5120 -> 13824 called back to back: 30.8 -> 29.0
+// us; one token, 4096 -> 32000: 24.4 -> 22.7 us.
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches with that attribute; cluster: CTAs of a cluster (1: none).
+template <class... P, class... A>
+cudaError_t launch_dense(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                         cudaStream_t s, const A&... args) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Calls f with the lb_dtype as a compile-time constant.
 template <class F>
 auto with_dtype(int t, F f) {

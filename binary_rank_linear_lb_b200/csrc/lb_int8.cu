@@ -28,11 +28,13 @@ constexpr int kGenTile = 64;
 constexpr int kGenPitch = 17;                // words of a staged row (16 used), odd: no bank conflicts
 
 template <int DT>
-__global__ void __launch_bounds__(256) int8_general_kernel(const Int8Args a) {
+__global__ void __launch_bounds__(256) int8_general_kernel(const __grid_constant__ Int8Args a) {
     __shared__ int xt[kGenTile * kGenPitch], wt[kGenTile * kGenPitch];
     const int n_m = (a.M + kGenTile - 1) / kGenTile;
     const int m0 = (int)(blockIdx.x % n_m) * kGenTile, n0 = (int)(blockIdx.x / n_m) * kGenTile;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    grid_trigger();
+    grid_wait();
     int acc[4][4] = {};
     for (int k0 = 0; k0 < a.K; k0 += 64) {
         for (int i = threadIdx.x; i < kGenTile * 64; i += 256) {
@@ -115,6 +117,8 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_kernel(const __grid_cons
     for (int i = 0; i < kFewCh; ++i) w[i] = a.w + (n0 + i < a.N ? n0 + i : a.N - 1) * a.ldw;
 #pragma unroll
     for (int m = 0; m < MT; ++m) x[m] = a.x + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
+    grid_trigger();
+    grid_wait();
     constexpr int kAhead = 2;                      // chunks requested together
     int c = c0 + lane;
     for (; c + 32 * (kAhead - 1) < c1; c += 32 * kAhead) {
@@ -174,10 +178,8 @@ cudaError_t launch_few(const Int8Args& a, int sms, cudaStream_t s) {
     while (parts < kFewWarps && groups * parts < (int64_t)sms * 24 && a.K / (parts * 2) >= 1024) parts *= 2;
     const int per_block = kFewWarps / parts;
     const unsigned blocks = (unsigned)((groups + per_block - 1) / per_block);
-    if (a.M == 1) int8_few_kernel<DT, 1><<<blocks, kFewThreads, 0, s>>>(a, parts);
-    else if (a.M == 2) int8_few_kernel<DT, 2><<<blocks, kFewThreads, 0, s>>>(a, parts);
-    else int8_few_kernel<DT, 4><<<blocks, kFewThreads, 0, s>>>(a, parts);
-    return cudaGetLastError();
+    auto kernel = a.M == 1 ? int8_few_kernel<DT, 1> : a.M == 2 ? int8_few_kernel<DT, 2> : int8_few_kernel<DT, 4>;
+    return launch_dense(kernel, blocks, kFewThreads, 0, 1, s, a, parts);
 }
 
 // ------------------------------------------------------------ tensor cores
@@ -392,6 +394,7 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
     const uint32_t full = s32(&ctl->full[0]), empty = s32(&ctl->empty[0]);
     const uint32_t acc_full = s32(&ctl->acc_full[0]), acc_empty = s32(&ctl->acc_empty[0]);
 
+    grid_trigger();
     // The loading warp sets up the stages' barriers and requests the first stages
     // before anything else; TMEM and the other barriers follow meanwhile.  (It and
     // the issuing warp run their loops whole, with one lane elected for the
@@ -427,6 +430,7 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncwarp();
+        grid_wait();
         for (int s = 0; s < stages && lt < n_tiles; ++s) load_stage();
     }
     if (warp == kIssueWarp) {
@@ -448,6 +452,7 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
     fence_before8();
     __syncthreads();
     fence_after8();
+    grid_wait();
     const uint32_t tmem = ctl->tmem_base;
 
     if (warp == kLoadWarp) {
@@ -623,6 +628,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     const uint32_t full = s32(&ctl->full[0]), empty = s32(&ctl->empty[0]);
     const uint32_t acc_full = s32(&ctl->acc_full[0]), acc_empty = s32(&ctl->acc_empty[0]);
 
+    grid_trigger();
     if (warp == kLoadWarp) {
         if (lane < stages) {
             mbar_init(full + 8u * (uint32_t)lane, 1);
@@ -650,6 +656,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     cluster_arrive8();
     cluster_wait8();                               // both CTAs' barriers are set up
     fence_after8();
+    grid_wait();
     const uint32_t tmem = ctl->tmem_base;
 
     if (warp == kLoadWarp) {
@@ -831,41 +838,23 @@ template <int DT, bool SPLIT, int KPER>
 cudaError_t launch_mma(const Int8Args& a, const MmaPlan& p, const CUtensorMap& wm, const CUtensorMap& xm,
                        int sms, cudaStream_t s) {
     const int64_t tiles = (int64_t)p.n_tok * p.n_ch;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1u << p.lg_split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles << p.lg_split : std::min<int64_t>(tiles, sms)));
-    cfg.blockDim = dim3(kMmaThreads);
-    cfg.dynamicSmemBytes = kMmaSmem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = SPLIT ? 1 : 0;
-    cudaError_t e = cudaFuncSetAttribute(int8_mma_kernel<DT, SPLIT, KPER>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
+    const cudaError_t e = cudaFuncSetAttribute(int8_mma_kernel<DT, SPLIT, KPER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
     if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&cfg, int8_mma_kernel<DT, SPLIT, KPER>, wm, xm, a, p);
+    return launch_dense(int8_mma_kernel<DT, SPLIT, KPER>,
+                        (unsigned)(SPLIT ? tiles << p.lg_split : std::min<int64_t>(tiles, sms)), kMmaThreads, kMmaSmem,
+                        1u << p.lg_split, s, wm, xm, a, p);
 }
 
 template <int DT, int KPER>
 cudaError_t launch_pair(const Int8Args& a, const MmaPlan& p, const CUtensorMap& wm, const CUtensorMap& xm,
                         int sms, cudaStream_t s) {
     const int64_t tiles = (int64_t)p.n_tok * p.n_ch;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, sms / 2)));
-    cfg.blockDim = dim3(kMmaThreads);
-    cfg.dynamicSmemBytes = kMmaSmem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaFuncSetAttribute(int8_pair_kernel<DT, KPER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
+    const cudaError_t e = cudaFuncSetAttribute(int8_pair_kernel<DT, KPER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
     if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&cfg, int8_pair_kernel<DT, KPER>, wm, xm, a, p);
+    return launch_dense(int8_pair_kernel<DT, KPER>, (unsigned)(2 * std::min<int64_t>(tiles, sms / 2)), kMmaThreads,
+                        kMmaSmem, 2, s, wm, xm, a, p);
 }
 
 // The tensor-core kernel reads rows through tensor maps: 16-byte pieces.
@@ -921,6 +910,8 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
         return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
     }
     const int64_t blocks = ((M + kGenTile - 1) / kGenTile) * ((out + kGenTile - 1) / kGenTile);
-    with_dtype(y_dtype, [&](auto d) { int8_general_kernel<d.value><<<(unsigned)blocks, 256, 0, s>>>(a); });
-    return cudaGetLastError() == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+    const cudaError_t e = with_dtype(y_dtype, [&](auto d) {
+        return launch_dense(int8_general_kernel<d.value>, (unsigned)blocks, 256, 0, 1, s, a);
+    });
+    return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
 }

@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
     const int p0 = SPLIT ? (int)((int64_t)n_pieces * rank / parts) : 0;
     const int p1 = SPLIT ? (int)((int64_t)n_pieces * (rank + 1) / parts) : n_pieces;
 
+    grid_trigger();
+    grid_wait();
     // the given token's logit is requested first
     int64_t tok = -1;
     float tok_x = 0.0f;
@@ -497,21 +499,8 @@ int row_parts(int64_t rows, int64_t vocab, int sms) {
 template <int DT>
 cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, int sms, cudaStream_t s) {
     const int parts = row_parts(rows, a.vocab, sms);
-    if (parts == 1) {
-        logprobs_kernel<DT, false><<<(unsigned)rows, kLpThreads, 0, s>>>(a, 1);
-        return cudaGetLastError();
-    }
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)parts;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * parts));
-    cfg.blockDim = dim3(kLpThreads);
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, true>, a, parts);
+    if (parts == 1) return launch_dense(logprobs_kernel<DT, false>, (unsigned)rows, kLpThreads, 0, 1, s, a, 1);
+    return launch_dense(logprobs_kernel<DT, true>, (unsigned)(rows * parts), kLpThreads, 0, (unsigned)parts, s, a, parts);
 }
 
 }  // namespace

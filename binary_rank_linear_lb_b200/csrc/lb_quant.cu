@@ -222,6 +222,8 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
     __shared__ unsigned long long exact_bits[WARP ? 8 : 1];
     const int tr = WARP ? 32 : (int)blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    grid_trigger();
+    grid_wait();
     if (WARP && row >= a.rows) return;
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
     const int apart = VEC ? 1 : tr;                // columns between a piece's elements
@@ -378,6 +380,8 @@ __global__ void __launch_bounds__(256) quant_wide_kernel(const __grid_constant__
     using X = Elem<DT>;
     __shared__ double red[32];
     const int64_t row = blockIdx.x;
+    grid_trigger();
+    grid_wait();
     if (a.residual) {
         const typename X::T* x = static_cast<const typename X::T*>(a.x) + row * a.ldx;
         const typename X::T* r = static_cast<const typename X::T*>(a.residual) + row * a.ldr;
@@ -388,29 +392,26 @@ __global__ void __launch_bounds__(256) quant_wide_kernel(const __grid_constant__
 }
 
 template <int DT, int C, bool VEC, int THREADS, bool NORM>
-void launch_block(const QuantArgs& a, cudaStream_t s) {
+cudaError_t launch_block(const QuantArgs& a, cudaStream_t s) {
     constexpr int per_thread = C * Piece<DT>::VE;
     const int threads = ((a.cols + per_thread - 1) / per_thread + 31) / 32 * 32;
-    quant_rows_kernel<DT, C, VEC, false, THREADS, NORM><<<(unsigned)a.rows, threads, 0, s>>>(a);
+    return launch_dense(quant_rows_kernel<DT, C, VEC, false, THREADS, NORM>, (unsigned)a.rows, threads, 0, 1, s, a);
 }
 
 template <int DT, bool VEC, bool NORM>
-void launch_rows(const QuantArgs& a, cudaStream_t s) {
+cudaError_t launch_rows(const QuantArgs& a, cudaStream_t s) {
     constexpr int kFull = 32 / Piece<DT>::VE;      // pieces of 32 elements
     constexpr int kFew = 8 / Piece<DT>::VE;        // pieces of 8 elements
     if (a.cols <= 32 * 32) {
         const unsigned blocks = (unsigned)((a.rows + 7) / 8);
-        if (a.cols <= 32 * 8) quant_rows_kernel<DT, kFew, VEC, true, 256, NORM><<<blocks, 256, 0, s>>>(a);
-        else quant_rows_kernel<DT, kFull, VEC, true, 256, NORM><<<blocks, 256, 0, s>>>(a);
-    } else if (a.cols <= kMaxThreads * 8 && a.rows <= kFewRows) {
-        launch_block<DT, kFew, VEC, kMaxThreads, NORM>(a, s);
-    } else if (a.cols <= 256 * 32) {
-        launch_block<DT, kFull, VEC, 256, NORM>(a, s);
-    } else if (a.cols <= kMaxThreads * 32) {
-        launch_block<DT, kFull, VEC, kMaxThreads, NORM>(a, s);
-    } else {
-        quant_wide_kernel<DT><<<(unsigned)a.rows, 256, 0, s>>>(a);
+        return a.cols <= 32 * 8
+                   ? launch_dense(quant_rows_kernel<DT, kFew, VEC, true, 256, NORM>, blocks, 256, 0, 1, s, a)
+                   : launch_dense(quant_rows_kernel<DT, kFull, VEC, true, 256, NORM>, blocks, 256, 0, 1, s, a);
     }
+    if (a.cols <= kMaxThreads * 8 && a.rows <= kFewRows) return launch_block<DT, kFew, VEC, kMaxThreads, NORM>(a, s);
+    if (a.cols <= 256 * 32) return launch_block<DT, kFull, VEC, 256, NORM>(a, s);
+    if (a.cols <= kMaxThreads * 32) return launch_block<DT, kFull, VEC, kMaxThreads, NORM>(a, s);
+    return launch_dense(quant_wide_kernel<DT>, (unsigned)a.rows, 256, 0, 1, s, a);
 }
 
 lb_status quant_call(QuantArgs a, int dt, cudaStream_t s) {
@@ -425,11 +426,11 @@ lb_status quant_call(QuantArgs a, int dt, cudaStream_t s) {
     a.weight_wide = is_aligned(a.weight, 16);
     // products that fp32 holds exactly: two 16-bit factors, or no weight
     a.inexact = a.weight && (dt == LB_F32 || a.weight_type == LB_F32);
-    with_dtype(dt, [&](auto d) {
-        if (a.norm) vec ? launch_rows<d.value, true, true>(a, s) : launch_rows<d.value, false, true>(a, s);
-        else vec ? launch_rows<d.value, true, false>(a, s) : launch_rows<d.value, false, false>(a, s);
+    const cudaError_t e = with_dtype(dt, [&](auto d) {
+        if (a.norm) return vec ? launch_rows<d.value, true, true>(a, s) : launch_rows<d.value, false, true>(a, s);
+        return vec ? launch_rows<d.value, true, false>(a, s) : launch_rows<d.value, false, false>(a, s);
     });
-    return cudaGetLastError() == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+    return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
 }
 
 bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
