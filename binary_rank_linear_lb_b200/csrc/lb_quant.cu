@@ -63,9 +63,7 @@ __device__ __forceinline__ float max_abs(float m, F2 v) {
     return r;
 }
 
-// With this many rows or fewer a row takes four times the threads (8 elements each
-// instead of 32): its latency is what the call waits for.
-constexpr int64_t kFewRows = 148;
+constexpr int64_t kFewElems = (int64_t)1 << 21;    // what the SMs hold at 8 elements a thread
 
 // The piece at p, n of its elements inside the row (the rest 0).  VEC: 16
 // consecutive bytes; otherwise (pointers or pitches that are not multiples of
@@ -190,23 +188,16 @@ __device__ __noinline__ void quant_row_64(const QuantArgs& a, int64_t row, int f
                    : (int8_t)code_d((double)X::get(s[i]), (double)weight_at(a.weight, a.weight_type, i), peak);
 }
 
-// The codes of a piece again, those near a border in 64 bits: from memory, one
-// by one (rare: a border is that near for one quotient in 16,000).
+// The code of column i again, in 64 bits (rare: a quotient that near a border
+// comes up once in 16,000, and for v = peak / 2).
 template <int DT>
-__device__ __noinline__ void settle_codes(const QuantArgs& a, int64_t row, int i, int apart, float inv,
-                                          double peak) {
+__device__ __noinline__ void settle_code(const QuantArgs& a, int64_t row, int i, double peak) {
     using X = Elem<DT>;
     const typename X::T* s = a.residual ? static_cast<const typename X::T*>(a.sum) + row * a.lds
                                         : static_cast<const typename X::T*>(a.x) + row * a.ldx;
-#pragma unroll 1
-    for (int e = 0; e < Piece<DT>::VE; ++e, i += apart) {
-        if (i >= a.cols) return;
-        const float sv = X::get(s[i]), w = weight_at(a.weight, a.weight_type, i);
-        const float f = sv * w * inv;
-        // (f is rounded here, so the check is a little wider: 127 * 2^-24 < 2^-16)
-        if (fabsf(f - rintf(f)) >= 0.5f - 1.5f * kBorder)
-            a.q[row * a.ldq + i] = (int8_t)code_d((double)sv, (double)w, peak);
-    }
+    if (i < a.cols)
+        a.q[row * a.ldq + i] =
+            (int8_t)code_d((double)X::get(s[i]), (double)weight_at(a.weight, a.weight_type, i), peak);
 }
 
 // C pieces of VE elements per thread; a warp per row (8 to a block) or a block
@@ -329,7 +320,12 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
     const F2 inv2 = f2(inv, inv), round2 = f2(kRound, kRound), back2 = f2(-kRound, -kRound);
     const F2 minus2 = f2(-1.0f, -1.0f);
     int8_t* q = a.q + row * a.ldq;
-    uint32_t near = 0;                             // pieces with a code near a border
+    // Elements with a code near a border, a bit each.  Where 127 / peak is exact (a peak
+    // of 127 * 2^n, common in 16-bit rows, with many values on borders) and so are the
+    // products, nothing is in doubt: the rounding above is that of the exact quotient.
+    const float limit = !a.inexact && fmaf(inv, peak, -127.0f) == 0.0f ? 1.0f : 0.5f - kBorder;
+    uint32_t near = 0;
+    static_assert(C * VE <= 32, "a bit for each element");
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = at(c), n = a.cols - i;
@@ -358,7 +354,14 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
             for (int e = 0; e < VE; ++e)
                 if (e * apart < n) q[i + e * apart] = (int8_t)code[e];
         }
-        near |= rest >= 0.5f - kBorder ? 1u << c : 0u;
+        if (rest >= limit)
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const F2 whole = mul2(add2(fma2(vc[j], inv2, round2), back2), minus2);
+                const float2 h = halves(fma2(vc[j], inv2, whole));
+                near |= (fabsf(h.x) >= limit ? 1u : 0u) << (c * VE + 2 * j);
+                near |= (fabsf(h.y) >= limit ? 1u : 0u) << (c * VE + 2 * j + 1);
+            }
     }
     double exact = (double)peak;
     if (NORM && a.inexact) {
@@ -367,9 +370,9 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
         exact = __longlong_as_double((long long)exact_bits[slot]);
     }
     while (near) {
-        const int c = __ffs(near) - 1;
+        const int b = __ffs(near) - 1;
         near &= near - 1;
-        settle_codes<DT>(a, row, at(c), apart, inv, exact);
+        settle_code<DT>(a, row, at(b / VE) + b % VE * apart, exact);
     }
 }
 
@@ -398,19 +401,33 @@ cudaError_t launch_block(const QuantArgs& a, cudaStream_t s) {
     return launch_dense(quant_rows_kernel<DT, C, VEC, false, THREADS, NORM>, (unsigned)a.rows, threads, 0, 1, s, a);
 }
 
+// Elements per thread.  Fewer mean more threads, so more of a row in flight and a
+// shorter path through it, but more of the work goes into the folds and, past 512
+// threads, an SM runs out of registers.  Measured (us, 8 / 16 / 32 elements, with
+// fp16 weights and a residual unless "plain"; the choice in brackets):
+//   333 x 5120 bf16 [5.5] 6.0 6.9, fp32 [6.6] 7.8 9.6, plain bf16 [3.0] 3.5 3.8;
+//   4096 x 4096 bf16 28.7 [25.2] 25.6, fp32 [37.7] 39.1 48.0, plain bf16 17.2 14.2 [12.7];
+//   4096 x 8192 bf16 58.0 46.8 [44.5], fp32 73.5 [70.5] 81.1, plain bf16 35.1 27.1 [23.6].
 template <int DT, bool VEC, bool NORM>
 cudaError_t launch_rows(const QuantArgs& a, cudaStream_t s) {
-    constexpr int kFull = 32 / Piece<DT>::VE;      // pieces of 32 elements
-    constexpr int kFew = 8 / Piece<DT>::VE;        // pieces of 8 elements
-    if (a.cols <= 32 * 32) {
+    constexpr int VE = Piece<DT>::VE;
+    constexpr bool kWide = DT == LB_F32;           // 32 elements are 8 pieces
+    if (a.cols <= 32 * 32) {                       // a warp per row
         const unsigned blocks = (unsigned)((a.rows + 7) / 8);
         return a.cols <= 32 * 8
-                   ? launch_dense(quant_rows_kernel<DT, kFew, VEC, true, 256, NORM>, blocks, 256, 0, 1, s, a)
-                   : launch_dense(quant_rows_kernel<DT, kFull, VEC, true, 256, NORM>, blocks, 256, 0, 1, s, a);
+                   ? launch_dense(quant_rows_kernel<DT, 8 / VE, VEC, true, 256, NORM>, blocks, 256, 0, 1, s, a)
+                   : launch_dense(quant_rows_kernel<DT, 32 / VE, VEC, true, 256, NORM>, blocks, 256, 0, 1, s, a);
     }
-    if (a.cols <= kMaxThreads * 8 && a.rows <= kFewRows) return launch_block<DT, kFew, VEC, kMaxThreads, NORM>(a, s);
-    if (a.cols <= 256 * 32) return launch_block<DT, kFull, VEC, 256, NORM>(a, s);
-    if (a.cols <= kMaxThreads * 32) return launch_block<DT, kFull, VEC, kMaxThreads, NORM>(a, s);
+    if (a.cols <= kMaxThreads * 8 && (a.rows * a.cols <= kFewElems || (NORM && kWide && a.cols <= 4096)))
+        return launch_block<DT, 8 / VE, VEC, kMaxThreads, NORM>(a, s);
+    if constexpr (NORM) {
+        if (a.cols <= (kWide ? 8192 : 6144)) return launch_block<DT, 16 / VE, VEC, 512, NORM>(a, s);
+        if constexpr (kWide)
+            if (a.cols <= kMaxThreads * 16) return launch_block<DT, 16 / VE, VEC, kMaxThreads, NORM>(a, s);
+    }
+    if constexpr (!(NORM && kWide))
+        if (a.cols <= 256 * 32) return launch_block<DT, 32 / VE, VEC, 256, NORM>(a, s);
+    if (a.cols <= kMaxThreads * 32) return launch_block<DT, 32 / VE, VEC, kMaxThreads, NORM>(a, s);
     return launch_dense(quant_wide_kernel<DT>, (unsigned)a.rows, 256, 0, 1, s, a);
 }
 
