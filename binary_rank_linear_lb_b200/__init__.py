@@ -352,93 +352,45 @@ def workspace_status(workspace: torch.Tensor, stream=None) -> int:
 
 
 # ------------------------------------------------------------------ dense path
-# The handle of the current stream of a device, and the current device.  (The public calls
-# build a Stream object, 3.4 us against 0.1 us, and check for initialisation: a tenth to a
-# third of the time of a one-token call.)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_empty = torch.empty_strided
+_marshal = None
 
 
-def _here(stream, dev: int, *tensors) -> Optional[int]:
-    """The handle to launch on when the call needs no other context than the present one
-    (no stream given, everything on the current GPU); None otherwise."""
-    if stream is not None or dev < 0 or dev != _current_device():
-        return None
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            return None
-    return _raw_stream(dev)
+def _dense():
+    """The dense path's marshalling (lb_torch.so; raises if it has not been built)."""
+    global _marshal
+    if _marshal is None:
+        lib()
+        try:
+            from . import lb_torch
+        except ImportError as e:
+            raise RuntimeError("lb_torch.so is missing or does not load: build it with "
+                               "`python -m binary_rank_linear_lb_b200.build`") from e
+        lb_torch.set_error(LbError)
+        _marshal = lb_torch
+    return _marshal
 
 
-def _elsewhere(stream, tensors, call):
-    """call() with the tensors' GPU as the current one and `stream` as its current stream.
+def _on_stream(stream, tensors, call):
+    """call() with `stream` (a torch stream or a handle) as the current one.
 
-    Checks that the tensors share one GPU.  With a stream other than the current one, what
-    the call allocates belongs to that stream, and the given tensors are marked as in use
-    there, so that their memory is not handed out again before the call has run.
+    What the call allocates belongs to that stream; where it is not the current one
+    already, the given tensors are marked as in use on it, so that their memory is not
+    handed out again before the call has run.
     """
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
-            raise ValueError(f"all tensors must be on one CUDA device, got {t.device} and "
-                             f"{tensors[0].device}")
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError(f"all tensors must be on one CUDA device, got {dev}")
     with torch.cuda.device(dev):
-        if stream is None:
-            return call()
         s = stream if hasattr(stream, "cuda_stream") else \
             torch.cuda.ExternalStream(int(stream), device=dev)
-        if s.device.index != dev:
-            raise ValueError(f"stream on {s.device}, tensors on {tensors[0].device}")
-        if s.cuda_stream != _raw_stream(dev):
+        if s.device != dev:
+            raise ValueError(f"stream on {s.device}, tensors on {dev}")
+        if s.cuda_stream != torch.cuda.current_stream().cuda_stream:
             for t in tensors:
                 if t is not None:
                     t.record_stream(s)
         with torch.cuda.stream(s):
             return call()
-
-
-def _rows(t: torch.Tensor, what: str) -> Tuple[int, int, int]:
-    """(rows, columns, row pitch) of a matrix whose rows are contiguous."""
-    if t.dim() == 2:
-        rows, cols = t.shape
-        if t.is_contiguous():
-            return rows, cols, cols
-        ld, unit = t.stride()
-        if unit == 1 or cols == 1:
-            return rows, cols, ld if rows > 1 else cols
-    raise ValueError(f"{what} must be a matrix with unit stride along its columns")
-
-
-def _dtype(t: torch.dtype, what: str) -> int:
-    dt = _DTYPES.get(t)
-    if dt is None:
-        raise ValueError(f"unsupported {what} dtype {t}")
-    return dt
-
-
-def _vector(t: torch.Tensor, n: int, dtype: Optional[torch.dtype], what: str) -> None:
-    if t.shape != (n,) or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what} must be a contiguous vector of {n}"
-                         + (f" {dtype}" if dtype is not None else "") + " elements")
-
-
-def _codes(q, scale, rows: int, cols: int, dev):
-    """(q, its pitch, scale), checked, or allocated where not given; a new q has a pitch of
-    whole 16-byte pieces, which linear_int8's fast kernels read."""
-    if q is None:
-        ldq = (cols + 15) // 16 * 16
-        q = _empty((rows, cols), (ldq, 1), dtype=torch.int8, device=dev)
-    else:
-        if q.dtype != torch.int8 or q.shape != (rows, cols):
-            raise ValueError(f"q must be an int8 matrix of {rows} x {cols}")
-        ldq = _rows(q, "q")[2]
-    if scale is None:
-        scale = _empty((rows,), (1,), dtype=torch.float32, device=dev)
-    else:
-        _vector(scale, rows, torch.float32, "scale")
-    return q, ldq, scale
 
 
 def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -449,15 +401,9 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     Used for head weights (a scale per output channel) and for activations (a scale per
     token).  A new q is a view whose pitch is a multiple of 16 bytes.
     """
-    st = _here(stream, x.get_device(), q, scale)
-    if st is None:
-        return _elsewhere(stream, (x, q, scale), lambda: quantize_rows(x, q, scale))
-    rows, cols, ldx = _rows(x, "x")
-    dt = _dtype(x.dtype, "x")
-    q, ldq, scale = _codes(q, scale, rows, cols, x.device)
-    _check(lib().lb_quantize_rows(x.data_ptr(), dt, rows, cols, ldx, q.data_ptr(), ldq,
-                                  scale.data_ptr(), st), "lb_quantize_rows")
-    return q, scale
+    if stream is not None:
+        return _on_stream(stream, (x, q, scale), lambda: quantize_rows(x, q, scale))
+    return (_marshal or _dense()).quantize_rows(x, q, scale)
 
 
 def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -470,34 +416,10 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
 
     ``sum_out`` receives s; it may be ``residual`` or ``x`` itself.
     """
-    st = _here(stream, x.get_device(), weight, residual, sum_out, q, scale)
-    if st is None:
-        return _elsewhere(stream, (x, weight, residual, sum_out, q, scale),
+    if stream is not None:
+        return _on_stream(stream, (x, weight, residual, sum_out, q, scale),
                           lambda: rmsnorm_quantize(x, weight, residual, eps, sum_out, q, scale))
-    rows, cols, ldx = _rows(x, "x")
-    dt = _dtype(x.dtype, "x")
-    wdt, ldr, lds = LB_F32, 0, 0
-    if weight is not None:
-        _vector(weight, cols, None, "weight")
-        wdt = _dtype(weight.dtype, "weight")
-    if residual is not None:
-        ldr = _rows(residual, "residual")[2]
-        if residual.dtype != x.dtype or residual.shape != x.shape:
-            raise ValueError("residual must have x's shape and dtype")
-        if sum_out is None:
-            lds = cols
-            sum_out = _empty((rows, cols), (cols, 1), dtype=x.dtype, device=x.device)
-        else:
-            lds = _rows(sum_out, "sum_out")[2]
-            if sum_out.dtype != x.dtype or sum_out.shape != x.shape:
-                raise ValueError("sum_out must have x's shape and dtype")
-    elif sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    q, ldq, scale = _codes(q, scale, rows, cols, x.device)
-    _check(lib().lb_rmsnorm_quantize(
-        x.data_ptr(), dt, rows, cols, ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight),
-        wdt, eps, q.data_ptr(), ldq, scale.data_ptr(), st), "lb_rmsnorm_quantize")
-    return q, scale, sum_out
+    return (_marshal or _dense()).rmsnorm_quantize(x, weight, residual, eps, sum_out, q, scale)
 
 
 def linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
@@ -508,26 +430,10 @@ def linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.
     ``xq`` (M x in) and ``wq`` (out x in) are int8 codes with fp32 scales per row, as
     quantize_rows and rmsnorm_quantize give them; ``dtype`` is that of a new y.
     """
-    st = _here(stream, xq.get_device(), xs, wq, ws, y)
-    if st is None:
-        return _elsewhere(stream, (xq, xs, wq, ws, y),
+    if stream is not None:
+        return _on_stream(stream, (xq, xs, wq, ws, y),
                           lambda: linear_int8(xq, xs, wq, ws, y, dtype))
-    M, k, ldx = _rows(xq, "xq")
-    n, kw, ldw = _rows(wq, "wq")
-    if xq.dtype != torch.int8 or wq.dtype != torch.int8 or k != kw:
-        raise ValueError("xq and wq must be int8 matrices with the same number of columns")
-    _vector(xs, M, torch.float32, "xs")
-    _vector(ws, n, torch.float32, "ws")
-    if y is None:
-        dt = _dtype(dtype, "y")
-        y, ldy = _empty((M, n), (n, 1), dtype=dtype, device=xq.device), n
-    else:
-        if y.shape != (M, n):
-            raise ValueError(f"y must be {M} x {n}")
-        dt, ldy = _dtype(y.dtype, "y"), _rows(y, "y")[2]
-    _check(lib().lb_linear_int8(xq.data_ptr(), ldx, xs.data_ptr(), M, wq.data_ptr(), ldw,
-                                ws.data_ptr(), k, n, y.data_ptr(), dt, ldy, st), "lb_linear_int8")
-    return y
+    return (_marshal or _dense()).linear_int8(xq, xs, wq, ws, y, dtype)
 
 
 class TokenLogprobs(NamedTuple):
@@ -544,27 +450,9 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     """lb_token_logprobs: log probabilities of ``tokens`` (int64, one per row; negative:
     none), entropy and the ``top`` (0 .. 32) most likely alternatives of logits
     (rows x vocab; -inf masks a token)."""
-    st = _here(stream, logits.get_device(), tokens)
-    if st is None:
-        return _elsewhere(stream, (logits, tokens), lambda: token_logprobs(logits, tokens, top))
-    rows, vocab, ld = _rows(logits, "logits")
-    dt = _dtype(logits.dtype, "logits")
-    top = int(top)
-    if not 0 <= top <= min(32, max(vocab, 1)):
-        raise ValueError(f"top must be 0 .. {min(32, vocab)}")
-    dev = logits.device
-    logprob = top_id = top_lp = None
-    if tokens is not None:
-        _vector(tokens, rows, torch.int64, "tokens")
-        logprob = _empty((rows,), (1,), dtype=torch.float32, device=dev)
-    entropy = _empty((rows,), (1,), dtype=torch.float32, device=dev)
-    if top:
-        top_id = _empty((rows, top), (top, 1), dtype=torch.int64, device=dev)
-        top_lp = _empty((rows, top), (top, 1), dtype=torch.float32, device=dev)
-    _check(lib().lb_token_logprobs(logits.data_ptr(), dt, rows, vocab, ld, _ptr(tokens),
-                                   _ptr(logprob), entropy.data_ptr(), top, _ptr(top_id),
-                                   _ptr(top_lp), st), "lb_token_logprobs")
-    return TokenLogprobs(logprob, entropy, top_id, top_lp)
+    if stream is not None:
+        return _on_stream(stream, (logits, tokens), lambda: token_logprobs(logits, tokens, top))
+    return TokenLogprobs._make((_marshal or _dense()).token_logprobs(logits, tokens, top))
 
 
 class Head:

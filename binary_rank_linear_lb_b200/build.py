@@ -3,7 +3,9 @@
     python -m binary_rank_linear_lb_b200.build [--verbose]
 
 Compiles every ``csrc/*.cu`` with nvcc for ``sm_100a`` only and links them into
-``binary_rank_linear_lb_b200/liblb.so``.  Runs without a GPU (nvcc cross-compiles).
+``binary_rank_linear_lb_b200/liblb.so``, and ``csrc/lb_torch.cpp`` (the dense path's argument
+marshalling for torch tensors) with g++ into ``lb_torch.so`` beside it.  Runs without a GPU
+(nvcc cross-compiles).
 """
 from __future__ import annotations
 
@@ -12,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblb.so")
+EXT = os.path.join(PKG, "lb_torch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -36,16 +40,49 @@ def deps():
         os.path.join(ROOT, "include", "lb.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def ext_deps():
+    return [os.path.join(CSRC, "lb_torch.cpp"), os.path.join(ROOT, "include", "lb.h")]
+
+
+def newer(target, sources_) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in sources_)
+
+
+def up_to_date() -> bool:
+    return newer(LIB, deps()) and newer(EXT, ext_deps())
+
+
+def build_ext() -> None:
+    """lb_torch.so, linked against the liblb.so beside it and the installed torch."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    tmp = EXT + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + os.path.join(ROOT, "include"),
+        "-I" + os.path.join(base, "include"),
+        "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"),
+        "-I" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"],
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        os.path.join(CSRC, "lb_torch.cpp"), "-o", tmp, "-L" + os.path.join(base, "lib"), "-lc10",
+        "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python", "-L" + PKG,
+        "-l:liblb.so", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, EXT)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
+    if force or not newer(LIB, deps()):
+        build_lib(verbose)
+    build_ext()
+    return LIB
+
+
+def build_lib(verbose: bool = False) -> None:
     out_dir = os.path.join(PKG, "_build")
     os.makedirs(out_dir, exist_ok=True)
     nvcc = nvcc_path()
@@ -63,7 +100,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcuda", "-lcublas",
                            "-lcusolver"])
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
