@@ -117,7 +117,7 @@ struct Stat {
 // Entries of cand[0 .. n) that come before `mine`.
 __device__ __forceinline__ int rank_of(unsigned long long mine, const unsigned long long* cand, int n) {
     int before = 0, o = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (; o + 1 < n; o += 2) {
         const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cand + o);
         before += (c.x > mine) + (c.y > mine);
@@ -302,42 +302,57 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
                 }
                 tied = T0 == lo && full > a.top + a.top / 4 + 1;
             }
-            // The logits >= from that the threads with a maximum >= from hold.  The warp
-            // reads such a thread's pieces together, a lane each (kTogether threads at a
-            // time): one round trip to L2 instead of one per batch.
-            constexpr int kTogether = 2;
+            // The logits >= from that the threads with a maximum >= from hold, read again:
+            // by the thread itself where it has a few pieces (they are in L1), else by
+            // its warp, a lane a piece and two threads at a time, which is one round
+            // trip to L2 instead of one per batch.
             auto gather = [&](uint32_t from) {
                 const float value = from == 0 ? -INFINITY : key_value(from);
-                uint32_t who = __ballot_sync(0xffffffffu, some && key >= from);
-                while (who) {
-                    const int l0 = __ffs(who) - 1;
-                    who &= who - 1;
-                    const int l1 = who ? __ffs(who) - 1 : -1;
-                    who &= who - 1;
-                    for (int off = p0 + warp * 32 + lane * kLpThreads; off - lane * kLpThreads < p1;
-                         off += 32 * kLpThreads) {
-                        uint4 r[kTogether];
-                        r[0] = load(off + l0);
-                        if (l1 >= 0) r[1] = load(off + l1);
+                auto scan = [&](const uint4& raw, int j) {
+                    F2 v[VE / 2];
+                    Piece<DT>::unpack(raw, v);
+                    float top = -INFINITY;
 #pragma unroll
-                        for (int w = 0; w < kTogether; ++w) {
-                            if (w == 1 && l1 < 0) break;
-                            const int j = off + (w ? l1 : l0), i = j * VE - shift;
-                            F2 v[VE / 2];
-                            Piece<DT>::unpack(r[w], v);
-                            float top = -INFINITY;
+                    for (int q = 0; q < VE / 2; ++q) top = max3_nan(top, v[q]);
+                    if (top < value) return;
+                    const int i = j * VE - shift;
 #pragma unroll
-                            for (int q = 0; q < VE / 2; ++q) top = max3_nan(top, v[q]);
-                            if (j >= p1 || top < value) continue;
-                            const T* e = reinterpret_cast<const T*>(&r[w]);
+                    for (int q = 0; q < VE; ++q) {
+                        const float2 h = halves(v[q / 2]);
+                        const float f = q & 1 ? h.y : h.x;
+                        if (f >= value && i + q >= 0 && i + q < a.vocab) {
+                            const int at = atomicAdd(&n_cand, 1);
+                            if (at < kCandidates) cand[at] = entry_of(order_key(f), i + q);
+                        }
+                    }
+                };
+                const bool mine = some && key >= from;
+                if (held <= 8 * kLpThreads) {
+                    if (mine)
+                        for (int j = p0 + (int)threadIdx.x; j < p1; j += 4 * kLpThreads) {
+                            uint4 r[4];
 #pragma unroll
-                            for (int q = 0; q < VE; ++q) {
-                                const uint32_t ek = order_key(X::get(e[q]));
-                                if (ek >= from && i + q >= 0 && i + q < a.vocab) {
-                                    const int at = atomicAdd(&n_cand, 1);
-                                    if (at < kCandidates) cand[at] = entry_of(ek, i + q);
-                                }
-                            }
+                            for (int w = 0; w < 4; ++w)
+                                if (j + w * kLpThreads < p1) r[w] = load(j + w * kLpThreads);
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                if (j + w * kLpThreads < p1) scan(r[w], j + w * kLpThreads);
+                        }
+                } else {
+                    uint32_t who = __ballot_sync(0xffffffffu, mine);
+                    while (who) {
+                        const int l0 = __ffs(who) - 1;
+                        who &= who - 1;
+                        const int l1 = who ? __ffs(who) - 1 : -1;
+                        who &= who - 1;
+                        for (int j = p0 + warp * 32 + lane * kLpThreads; j - lane * kLpThreads < p1;
+                             j += 32 * kLpThreads) {
+                            const bool b0 = j + l0 < p1, b1 = l1 >= 0 && j + l1 < p1;
+                            uint4 r0, r1;
+                            if (b0) r0 = load(j + l0);
+                            if (b1) r1 = load(j + l1);
+                            if (b0) scan(r0, j + l0);
+                            if (b1) scan(r1, j + l1);
                         }
                     }
                 }
