@@ -34,6 +34,7 @@ constexpr int kMaxTop = 32;
 constexpr int kGroups = 64;                  // groups of four threads
 constexpr int kCandidates = 1024;            // logits >= T kept at most
 constexpr int kLpCluster = 8;
+static_assert(kLpCluster / 2 <= kLpWarps - 1, "a warp merges two lists, the last folds the sums");
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // t below this is as good as -inf (2^t is 0), and unlike it can be multiplied by 0.
@@ -123,6 +124,18 @@ __device__ __forceinline__ int rank_of(unsigned long long mine, const unsigned l
         before += (c.x > mine) + (c.y > mine);
     }
     return o < n ? before + (cand[o] > mine) : before;
+}
+
+// The 32 largest of two falling lists of 32, in order: u holds the first, v the
+// second from its end (their larger elements, lane by lane, are bitonic).
+__device__ __forceinline__ unsigned long long merge_sorted(unsigned long long u, unsigned long long v) {
+    unsigned long long x = u > v ? u : v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long y = __shfl_xor_sync(0xffffffffu, x, o);
+        x = (threadIdx.x & o) ? (x < y ? x : y) : (x > y ? x : y);
+    }
+    return x;
 }
 
 // What a CTA knows of its part of a row.
@@ -445,14 +458,26 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
         cluster_sync();
         if (rank == 0) {
             const uint32_t base = (uint32_t)__cvta_generic_to_shared(&part);
-            const int n = parts * a.top;
-            unsigned long long mine = 0;
-            if ((int)threadIdx.x < n)                                       // (8 parts of 32: one each)
-                mine = ld_peer64(peer(base + (uint32_t)offsetof(LpPart, list) + 8u * (threadIdx.x % a.top),
-                                      threadIdx.x / a.top));
+            // the lists, in pairs: warp w merges those of CTAs 2w and 2w + 1, and so on
+            if (a.top > 0) {
+                unsigned long long best = 0;
+                if (2 * warp < parts) {
+                    const uint32_t la = base + (uint32_t)offsetof(LpPart, list);
+                    const unsigned long long u = lane < a.top ? ld_peer64(peer(la + 8u * lane, 2 * warp)) : 0;
+                    const unsigned long long v = 31 - lane < a.top ? ld_peer64(peer(la + 8u * (31 - lane), 2 * warp + 1)) : 0;
+                    best = merge_sorted(u, v);
+                }
+                for (int n = parts / 2; n > 1; n /= 2) {             // n lists left, one a warp
+                    if (warp < n) cand[32 * warp + lane] = best;
+                    __syncthreads();
+                    if (2 * warp < n) best = merge_sorted(cand[64 * warp + lane], cand[64 * warp + 63 - lane]);
+                    __syncthreads();
+                }
+                if (warp == 0) cand[lane] = best;
+            }
             float pm = -INFINITY, pS = 0.0f, pA = 0.0f;
             int pn = 0;
-            if (threadIdx.x < 32) {
+            if (warp == kLpWarps - 1) {
                 if (lane < parts) {
                     pm = __uint_as_float(ld_peer32(peer(base + (uint32_t)offsetof(LpPart, m), lane)));
                     pS = __uint_as_float(ld_peer32(peer(base + (uint32_t)offsetof(LpPart, S), lane)));
@@ -476,13 +501,8 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
                 pm = all;
             }
             __syncthreads();                                                // part is read by this CTA too
-            if ((int)threadIdx.x < n) cand[threadIdx.x] = mine;
-            if (threadIdx.x == 0) { part.m = pm; part.S = pS; part.A = pA; part.nan = pn; }
-            __syncthreads();
-            if (mine != 0) {
-                const int before = rank_of(mine, cand, n);
-                if (before < a.top) part.list[before] = mine;
-            }
+            if ((int)threadIdx.x < a.top) part.list[threadIdx.x] = cand[threadIdx.x];
+            if (threadIdx.x == kLpThreads - 32) { part.m = pm; part.S = pS; part.A = pA; part.nan = pn; }
             __syncthreads();
         }
         cluster_sync();                                                     // (the others' parts have been read)
