@@ -37,6 +37,7 @@ struct QuantArgs {
     int norm;                 // 0: no norm (size 1)
     int weight_type;          // lb_dtype of weight
     bool weight_wide;         // weight is 16-byte aligned
+    bool q_wide;              // so are the codes of every piece, to their size
     bool inexact;             // s w can need more than fp32's 24 bits
     float eps;
 };
@@ -65,33 +66,78 @@ __device__ __forceinline__ float max_abs(float m, F2 v) {
 
 constexpr int64_t kFewElems = (int64_t)1 << 21;    // what the SMs hold at 8 elements a thread
 
-// The piece at p, n of its elements inside the row (the rest 0).  VEC: 16
-// consecutive bytes; otherwise (pointers or pitches that are not multiples of
-// 16) elements `apart` columns from each other.
-template <int DT, bool VEC>
-__device__ __forceinline__ uint4 load_piece(const typename Elem<DT>::T* p, int n, int apart) {
+// Bytes m .. m + 15 of the 32 in lo, hi (0 < m < 16, the same for the whole row).
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, int m) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 7; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
+    const uint32_t bits = 8u * (uint32_t)(m & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// The piece of VE elements from column i of a row (zeros past its end).  A row
+// that does not start on 16 bytes is read in aligned 16-byte pairs that lie inside
+// it and shifted; its ends element by element.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ uint4 load_piece(const typename Elem<DT>::T* row, int i, int cols) {
     using T = typename Elem<DT>::T;
     constexpr int VE = Piece<DT>::VE;
-    if (VEC && n >= VE) return *reinterpret_cast<const uint4*>(p);
+    const T* p = row + i;
+    const int m = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    if (i + VE <= cols) {
+        if (m == 0) return *reinterpret_cast<const uint4*>(p);
+        const int before = m / (int)sizeof(T);     // elements of the pair before the piece
+        if (!ALIGNED && i >= before && i - before + 2 * VE <= cols) {
+            const uint4* q = reinterpret_cast<const uint4*>(p - before);
+            return shifted(q[0], q[1], m);
+        }
+    }
     uint4 u = make_uint4(0u, 0u, 0u, 0u);
     T* e = reinterpret_cast<T*>(&u);
 #pragma unroll
-    for (int i = 0; i < VE; ++i)
-        if (i * (VEC ? 1 : apart) < n) e[i] = p[VEC ? i : i * apart];
+    for (int k = 0; k < VE; ++k)
+        if (i + k < cols) e[k] = p[k];
     return u;
 }
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_piece(typename Elem<DT>::T* p, int n, int apart, uint4 u) {
+
+// Stores it.  Called by whole warps, lanes holding consecutive pieces: where the row
+// is not aligned, a lane stores the aligned 16 bytes that end inside its piece (the
+// lane before it gives the start), and what no such store covers goes element by element.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void store_piece(typename Elem<DT>::T* row, int i, int cols, uint4 u) {
     using T = typename Elem<DT>::T;
     constexpr int VE = Piece<DT>::VE;
-    if (VEC && n >= VE) {
-        *reinterpret_cast<uint4*>(p) = u;
-        return;
-    }
+    T* p = row + i;
     const T* e = reinterpret_cast<const T*>(&u);
+    const bool whole = i + VE <= cols;
+    int from = 0, to = VE;                         // elements left to store one by one
+    if constexpr (ALIGNED) {
+        if (whole) {
+            *reinterpret_cast<uint4*>(p) = u;
+            return;
+        }
+    } else {
+        const int lane = threadIdx.x & 31, m = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+        const int head = m ? (16 - m) / (int)sizeof(T) : VE;       // elements up to the next 16 bytes
+        const uint4 prev = make_uint4(__shfl_up_sync(0xffffffffu, u.x, 1), __shfl_up_sync(0xffffffffu, u.y, 1),
+                                      __shfl_up_sync(0xffffffffu, u.z, 1), __shfl_up_sync(0xffffffffu, u.w, 1));
+        const bool next = __shfl_down_sync(0xffffffffu, whole ? 1 : 0, 1) != 0 && lane < 31;
+        if (whole && m == 0) {
+            *reinterpret_cast<uint4*>(p) = u;
+            return;
+        }
+        if (whole && lane > 0) {                   // the last m bytes of the piece before, then this one's first
+            *reinterpret_cast<uint4*>(p - m / (int)sizeof(T)) = shifted(prev, u, 16 - m);
+            from = head;
+        }
+        if (whole && next) to = head;
+    }
 #pragma unroll
-    for (int i = 0; i < VE; ++i)
-        if (i * (VEC ? 1 : apart) < n) p[VEC ? i : i * apart] = e[i];
+    for (int k = 0; k < VE; ++k)
+        if (k >= from && k < to && i + k < cols) p[k] = e[k];
 }
 
 __device__ __forceinline__ float weight_at(const void* w, int wt, int i) {
@@ -101,9 +147,9 @@ __device__ __forceinline__ float weight_at(const void* w, int wt, int i) {
     return static_cast<const float*>(w)[i];
 }
 // The weights of the piece of VE columns from i, as pairs.
-template <int VE, bool VEC>
-__device__ __forceinline__ void load_weights(const QuantArgs& a, int i, int n, int apart, F2 (&v)[VE / 2]) {
-    if (VEC && a.weight_wide && n >= VE) {
+template <int VE>
+__device__ __forceinline__ void load_weights(const QuantArgs& a, int i, F2 (&v)[VE / 2]) {
+    if (a.weight_wide && i + VE <= a.cols) {
         if (a.weight_type == LB_F32) {
 #pragma unroll
             for (int j = 0; j < VE; j += 4) {
@@ -127,14 +173,10 @@ __device__ __forceinline__ void load_weights(const QuantArgs& a, int i, int n, i
         }
         return;
     }
-    float e[VE];
 #pragma unroll
-    for (int j = 0; j < VE; ++j) {
-        const int o = VEC ? j : j * apart;
-        e[j] = o < n ? weight_at(a.weight, a.weight_type, i + o) : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < VE; j += 2) v[j / 2] = f2(e[j], e[j + 1]);
+    for (int j = 0; j < VE; j += 2)
+        v[j / 2] = f2(i + j < a.cols ? weight_at(a.weight, a.weight_type, i + j) : 0.0f,
+                      i + j + 1 < a.cols ? weight_at(a.weight, a.weight_type, i + j + 1) : 0.0f);
 }
 
 // Folds over the threads of a row: a warp (red unused) or the block.
@@ -205,7 +247,7 @@ __device__ __noinline__ void settle_code(const QuantArgs& a, int64_t row, int i,
 // element comes and goes with 3 to 7 bytes), so everything runs on pairs and the
 // codes take two pair instructions: v * 127 / peak + kRound holds the code in its
 // low byte, and what it left over says how near the border was.
-template <int DT, int C, bool VEC, bool WARP, int THREADS, bool NORM>
+template <int DT, int C, bool ALIGNED, bool WARP, int THREADS, bool NORM>
 __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int VE = Piece<DT>::VE, P = VE / 2;
@@ -217,25 +259,24 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
     grid_wait();
     if (WARP && row >= a.rows) return;
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    const int apart = VEC ? 1 : tr;                // columns between a piece's elements
-    auto at = [&](int c) { return VEC ? (c * tr + t) * VE : c * tr * VE + t; };   // a piece's first column
+    auto at = [&](int c) { return (c * tr + t) * VE; };              // a piece's first column
 
     uint4 raw[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) raw[c] = load_piece<DT, VEC>(x + at(c), a.cols - at(c), apart);
+    for (int c = 0; c < C; ++c) raw[c] = load_piece<DT, ALIGNED>(x, at(c), a.cols);
     // with 8 elements a thread (few rows) the weights are requested with the row
     constexpr bool kEarly = NORM && C * VE == 8;
     F2 we[kEarly ? C : 1][P];
     if constexpr (kEarly)
         if (a.weight)
 #pragma unroll
-            for (int c = 0; c < C; ++c) load_weights<VE, VEC>(a, at(c), a.cols - at(c), apart, we[c]);
+            for (int c = 0; c < C; ++c) load_weights<VE>(a, at(c), we[c]);
     if (NORM && a.residual) {
         const T* r = static_cast<const T*>(a.residual) + row * a.ldr;
         T* sum = static_cast<T*>(a.sum) + row * a.lds;
         uint4 more[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) more[c] = load_piece<DT, VEC>(r + at(c), a.cols - at(c), apart);
+        for (int c = 0; c < C; ++c) more[c] = load_piece<DT, ALIGNED>(r, at(c), a.cols);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             F2 xv[P], rv[P];
@@ -244,7 +285,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
 #pragma unroll
             for (int i = 0; i < P; ++i) xv[i] = add2(xv[i], rv[i]);
             raw[c] = Piece<DT>::pack(xv);
-            store_piece<DT, VEC>(sum + at(c), a.cols - at(c), apart, raw[c]);
+            store_piece<DT, ALIGNED>(sum, at(c), a.cols, raw[c]);
         }
     }
     // v = s w, the sum of s^2 and the largest |v|.  (Without a norm v is the row
@@ -262,7 +303,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
             for (int i = 0; i < P; ++i) sq = fma2(vc[i], vc[i], sq);
             if (a.weight) {
                 F2 w[P];
-                if constexpr (!kEarly) load_weights<VE, VEC>(a, at(c), a.cols - at(c), apart, w);
+                if constexpr (!kEarly) load_weights<VE>(a, at(c), w);
 #pragma unroll
                 for (int i = 0; i < P; ++i) vc[i] = mul2(vc[i], kEarly ? we[c][i] : w[i]);
             }
@@ -306,7 +347,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
                 if (fmaxf(fabsf(h.x), fabsf(h.y)) == peak)
 #pragma unroll 1
                     for (int e = 0; e < 2; ++e) {
-                        const int o = at(c) + (2 * i + e) * apart;
+                        const int o = at(c) + 2 * i + e;
                         if (o < a.cols)          // (non-negative doubles order like their bits)
                             atomicMax(&exact_bits[slot],
                                       (unsigned long long)__double_as_longlong(fabs(
@@ -342,7 +383,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
             const F2 whole = mul2(add2(k, back2), minus2);
             rest = max_abs(rest, fma2(vc[j], inv2, whole));
         }
-        if (VEC && n >= VE) {
+        if (a.q_wide && n >= VE) {
             uint32_t w[VE / 4];
 #pragma unroll
             for (int e = 0; e < VE; e += 4)
@@ -352,7 +393,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
         } else {
 #pragma unroll
             for (int e = 0; e < VE; ++e)
-                if (e * apart < n) q[i + e * apart] = (int8_t)code[e];
+                if (e < n) q[i + e] = (int8_t)code[e];
         }
         if (rest >= limit)
 #pragma unroll
@@ -372,7 +413,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
     while (near) {
         const int b = __ffs(near) - 1;
         near &= near - 1;
-        settle_code<DT>(a, row, at(b / VE) + b % VE * apart, exact);
+        settle_code<DT>(a, row, at(b / VE) + b % VE, exact);
     }
 }
 
@@ -394,11 +435,11 @@ __global__ void __launch_bounds__(256) quant_wide_kernel(const __grid_constant__
     quant_row_64<DT, false>(a, row, threadIdx.x, 256, red);
 }
 
-template <int DT, int C, bool VEC, int THREADS, bool NORM>
+template <int DT, int C, bool ALIGNED, int THREADS, bool NORM>
 cudaError_t launch_block(const QuantArgs& a, cudaStream_t s) {
     constexpr int per_thread = C * Piece<DT>::VE;
     const int threads = ((a.cols + per_thread - 1) / per_thread + 31) / 32 * 32;
-    return launch_dense(quant_rows_kernel<DT, C, VEC, false, THREADS, NORM>, (unsigned)a.rows, threads, 0, 1, s, a);
+    return launch_dense(quant_rows_kernel<DT, C, ALIGNED, false, THREADS, NORM>, (unsigned)a.rows, threads, 0, 1, s, a);
 }
 
 // Elements per thread.  Fewer mean more threads, so more of a row in flight and a
@@ -408,26 +449,26 @@ cudaError_t launch_block(const QuantArgs& a, cudaStream_t s) {
 //   333 x 5120 bf16 [5.5] 6.0 6.9, fp32 [6.6] 7.8 9.6, plain bf16 [3.0] 3.5 3.8;
 //   4096 x 4096 bf16 28.7 [25.2] 25.6, fp32 [37.7] 39.1 48.0, plain bf16 17.2 14.2 [12.7];
 //   4096 x 8192 bf16 58.0 46.8 [44.5], fp32 73.5 [70.5] 81.1, plain bf16 35.1 27.1 [23.6].
-template <int DT, bool VEC, bool NORM>
+template <int DT, bool ALIGNED, bool NORM>
 cudaError_t launch_rows(const QuantArgs& a, cudaStream_t s) {
     constexpr int VE = Piece<DT>::VE;
     constexpr bool kWide = DT == LB_F32;           // 32 elements are 8 pieces
     if (a.cols <= 32 * 32) {                       // a warp per row
         const unsigned blocks = (unsigned)((a.rows + 7) / 8);
         return a.cols <= 32 * 8
-                   ? launch_dense(quant_rows_kernel<DT, 8 / VE, VEC, true, 256, NORM>, blocks, 256, 0, 1, s, a)
-                   : launch_dense(quant_rows_kernel<DT, 32 / VE, VEC, true, 256, NORM>, blocks, 256, 0, 1, s, a);
+                   ? launch_dense(quant_rows_kernel<DT, 8 / VE, ALIGNED, true, 256, NORM>, blocks, 256, 0, 1, s, a)
+                   : launch_dense(quant_rows_kernel<DT, 32 / VE, ALIGNED, true, 256, NORM>, blocks, 256, 0, 1, s, a);
     }
     if (a.cols <= kMaxThreads * 8 && (a.rows * a.cols <= kFewElems || (NORM && kWide && a.cols <= 4096)))
-        return launch_block<DT, 8 / VE, VEC, kMaxThreads, NORM>(a, s);
+        return launch_block<DT, 8 / VE, ALIGNED, kMaxThreads, NORM>(a, s);
     if constexpr (NORM) {
-        if (a.cols <= (kWide ? 8192 : 6144)) return launch_block<DT, 16 / VE, VEC, 512, NORM>(a, s);
+        if (a.cols <= (kWide ? 8192 : 6144)) return launch_block<DT, 16 / VE, ALIGNED, 512, NORM>(a, s);
         if constexpr (kWide)
-            if (a.cols <= kMaxThreads * 16) return launch_block<DT, 16 / VE, VEC, kMaxThreads, NORM>(a, s);
+            if (a.cols <= kMaxThreads * 16) return launch_block<DT, 16 / VE, ALIGNED, kMaxThreads, NORM>(a, s);
     }
     if constexpr (!(NORM && kWide))
-        if (a.cols <= 256 * 32) return launch_block<DT, 32 / VE, VEC, 256, NORM>(a, s);
-    if (a.cols <= kMaxThreads * 32) return launch_block<DT, 32 / VE, VEC, kMaxThreads, NORM>(a, s);
+        if (a.cols <= 256 * 32) return launch_block<DT, 32 / VE, ALIGNED, 256, NORM>(a, s);
+    if (a.cols <= kMaxThreads * 32) return launch_block<DT, 32 / VE, ALIGNED, kMaxThreads, NORM>(a, s);
     return launch_dense(quant_wide_kernel<DT>, (unsigned)a.rows, 256, 0, 1, s, a);
 }
 
@@ -436,16 +477,15 @@ lb_status quant_call(QuantArgs a, int dt, cudaStream_t s) {
     const lb_status st = dense_device(sms);
     if (st != LB_OK) return st;
     const int64_t per16 = 16 / (int64_t)dtype_size(dt);        // elements in 16 bytes
-    const bool vec = is_aligned(a.x, 16) && is_aligned(a.residual, 16) && is_aligned(a.sum, 16) &&
-                     is_aligned(a.q, (size_t)per16) &&
-                     (a.rows == 1 || (a.ldx % per16 == 0 && a.ldr % per16 == 0 && a.lds % per16 == 0 &&
-                                      a.ldq % per16 == 0));
+    const bool aligned = is_aligned(a.x, 16) && is_aligned(a.residual, 16) && is_aligned(a.sum, 16) &&
+                         (a.rows == 1 || (a.ldx % per16 == 0 && a.ldr % per16 == 0 && a.lds % per16 == 0));
+    a.q_wide = is_aligned(a.q, (size_t)per16) && (a.rows == 1 || a.ldq % per16 == 0);
     a.weight_wide = is_aligned(a.weight, 16);
     // products that fp32 holds exactly: two 16-bit factors, or no weight
     a.inexact = a.weight && (dt == LB_F32 || a.weight_type == LB_F32);
     const cudaError_t e = with_dtype(dt, [&](auto d) {
-        if (a.norm) return vec ? launch_rows<d.value, true, true>(a, s) : launch_rows<d.value, false, true>(a, s);
-        return vec ? launch_rows<d.value, true, false>(a, s) : launch_rows<d.value, false, false>(a, s);
+        if (a.norm) return aligned ? launch_rows<d.value, true, true>(a, s) : launch_rows<d.value, false, true>(a, s);
+        return aligned ? launch_rows<d.value, true, false>(a, s) : launch_rows<d.value, false, false>(a, s);
     });
     return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
 }
