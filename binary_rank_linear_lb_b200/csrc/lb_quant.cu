@@ -96,6 +96,7 @@ __device__ __forceinline__ uint4 load_piece(const typename Elem<DT>::T* row, int
         }
     }
     uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (i >= cols) return u;
     T* e = reinterpret_cast<T*>(&u);
 #pragma unroll
     for (int k = 0; k < VE; ++k)
@@ -135,9 +136,10 @@ __device__ __forceinline__ void store_piece(typename Elem<DT>::T* row, int i, in
         }
         if (whole && next) to = head;
     }
+    if (i < cols)
 #pragma unroll
-    for (int k = 0; k < VE; ++k)
-        if (k >= from && k < to && i + k < cols) p[k] = e[k];
+        for (int k = 0; k < VE; ++k)
+            if (k >= from && k < to && i + k < cols) p[k] = e[k];
 }
 
 __device__ __forceinline__ float weight_at(const void* w, int wt, int i) {
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
                 w[e / 4] = prmt(prmt(code[e], code[e + 1], 0x0040u), prmt(code[e + 2], code[e + 3], 0x0040u), 0x5410u);
             if constexpr (VE == 8) *reinterpret_cast<uint2*>(q + i) = make_uint2(w[0], w[1]);
             else *reinterpret_cast<uint32_t*>(q + i) = w[0];
-        } else {
+        } else if (n > 0) {
 #pragma unroll
             for (int e = 0; e < VE; ++e)
                 if (e < n) q[i + e] = (int8_t)code[e];
@@ -454,10 +456,10 @@ cudaError_t launch_rows(const QuantArgs& a, cudaStream_t s) {
     constexpr int VE = Piece<DT>::VE;
     constexpr bool kWide = DT == LB_F32;           // 32 elements are 8 pieces
     if (a.cols <= 32 * 32) {                       // a warp per row
-        const unsigned blocks = (unsigned)((a.rows + 7) / 8);
-        return a.cols <= 32 * 8
-                   ? launch_dense(quant_rows_kernel<DT, 8 / VE, ALIGNED, true, 256, NORM>, blocks, 256, 0, 1, s, a)
-                   : launch_dense(quant_rows_kernel<DT, 32 / VE, ALIGNED, true, 256, NORM>, blocks, 256, 0, 1, s, a);
+        auto kernel = a.cols <= 32 * 8    ? quant_rows_kernel<DT, 8 / VE, ALIGNED, true, 256, NORM>
+                      : a.cols <= 32 * 16 ? quant_rows_kernel<DT, 16 / VE, ALIGNED, true, 256, NORM>
+                                          : quant_rows_kernel<DT, 32 / VE, ALIGNED, true, 256, NORM>;
+        return launch_dense(kernel, (unsigned)((a.rows + 7) / 8), 256, 0, 1, s, a);
     }
     if (a.cols <= kMaxThreads * 8 && (a.rows * a.cols <= kFewElems || (NORM && kWide && a.cols <= 4096)))
         return launch_block<DT, 8 / VE, ALIGNED, kMaxThreads, NORM>(a, s);
