@@ -378,8 +378,9 @@ def _on_stream(stream, tensors, call):
     handed out again before the call has run.
     """
     dev = tensors[0].device
-    if dev.type != "cuda":
-        raise ValueError(f"all tensors must be on one CUDA device, got {dev}")
+    for t in tensors:
+        if t is not None and (t.device != dev or dev.type != "cuda"):
+            raise ValueError(f"all tensors must be on one CUDA device, got {t.device} and {dev}")
     with torch.cuda.device(dev):
         s = stream if hasattr(stream, "cuda_stream") else \
             torch.cuda.ExternalStream(int(stream), device=dev)

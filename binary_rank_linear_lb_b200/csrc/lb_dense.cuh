@@ -136,7 +136,8 @@ inline lb_status dense_device(int& sms) {
 // on a stream; each lets the next one start while it still runs (grid_trigger),
 // and touches global memory only after everything before it has completed and is
 // visible (every thread calls grid_wait before its first access), so only launch
-// latency and set-up overlap.  333 x 5120 -> 13824 called back to back: 30.8 -> 29.0
+// latency and set-up overlap.  What a kernel reads may thus be written while it
+// already runs, so it is read with ordinary loads, none through the read-only path.  333 x 5120 -> 13824 called back to back: 30.8 -> 29.0
 // us; one token, 4096 -> 32000: 24.4 -> 22.7 us.
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

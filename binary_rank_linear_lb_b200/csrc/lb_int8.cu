@@ -78,11 +78,16 @@ __global__ void __launch_bounds__(256) int8_general_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------ few tokens
-// One to four tokens: the weights stream past once and __dp4a keeps up (M products
-// of four per weight word, against 64 a clock and SM).  A warp takes four
-// channels and, with few channels, a block's warps share their K (`parts`), so
-// that every SM has some 100 KB of weights in flight; a lane holds 16 bytes of
-// every row, 512 contiguous bytes a warp.  xq comes from L1.
+// One or two tokens, and up to four over a small weight: the weights stream past
+// once and __dp4a keeps up (M products of four per weight word, against 64 a clock
+// and SM).  A warp takes four channels and, with few channels, a block's warps
+// share their K (`parts`), so that every SM has some 100 KB of weights in flight;
+// a lane holds 16 bytes of every row, 512 contiguous bytes a warp.  xq comes from L1.
+//
+// Against the tensor cores (us): 4096 -> 32000, one token 22.9 / 23.1, two 24.9 /
+// 24.7, four 29.4 / 24.7; 4096 -> 4096, one 5.2 / 6.1, four 6.8 / 6.1 (the set-up
+// of barriers, TMEM and tensor maps); 1024 -> 1024, one 2.4 / 4.8, four 2.6 / 4.8.
+// What bounds it: HBM, 5.8 TB/s (90% of the copy rate) at one token, 4096 -> 32000.
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kFewCh = 4;                          // channels of a warp
@@ -96,7 +101,7 @@ __device__ __forceinline__ int dot16(int4 a, int4 b, int acc) {
 }
 __device__ __forceinline__ int4 ld_once(const int8_t* p) {
     int4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_kernel(const __grid_cons
         for (int u = 0; u < kAhead; ++u)
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const int4 xv = __ldg(reinterpret_cast<const int4*>(x[m]) + c + 32 * u);
+                const int4 xv = reinterpret_cast<const int4*>(x[m])[c + 32 * u];
 #pragma unroll
                 for (int i = 0; i < kFewCh; ++i) acc[i][m] = dot16(wv[u][i], xv, acc[i][m]);
             }
@@ -141,13 +146,14 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_kernel(const __grid_cons
         for (int i = 0; i < kFewCh; ++i) {
             const int4 wv = ld_once(w[i] + 16 * (int64_t)c);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[i][m] = dot16(wv, __ldg(reinterpret_cast<const int4*>(x[m]) + c), acc[i][m]);
+            for (int m = 0; m < MT; ++m) acc[i][m] = dot16(wv, reinterpret_cast<const int4*>(x[m])[c], acc[i][m]);
         }
     if (part == parts - 1 && lane < a.K - 16 * chunks)           // the last bytes, one a lane
 #pragma unroll
         for (int i = 0; i < kFewCh; ++i)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[i][m] += (int)w[i][16 * chunks + lane] * (int)x[m][16 * chunks + lane];
+            for (int m = 0; m < MT; ++m)
+                acc[i][m] += (int)w[i][16 * chunks + lane] * (int)x[m][16 * chunks + lane];
 #pragma unroll
     for (int i = 0; i < kFewCh; ++i)
 #pragma unroll
@@ -194,6 +200,11 @@ cudaError_t launch_few(const Int8Args& a, int sms, cudaStream_t s) {
 // the accumulators, warp 8 loads (TMA, 128 bytes of K a stage, 128-byte swizzle;
 // zeros past the edges), warp 9 owns TMEM and issues the MMAs.  Two accumulators:
 // one tile is drained while the next is summed.
+//
+// What bounds it: HBM while the tokens are few (16 x 8192 -> 28672 bf16: 40.4 us, 5.8
+// TB/s, 90% of the copy rate), then what L2 gives an SM (see mma_plan), then the
+// MMAs and the card's power limit (4096 x 8192 -> 32000, pairs of CTAs: 672 us, 3190
+// TOP/s in a burst, 95% of twice the bf16 burst rate; some 770 us when it runs on).
 //
 // With few tiles the K blocks of a tile are split over a cluster of CTAs, which
 // exchange their partial sums through distributed shared memory (each CTA folds
@@ -340,9 +351,9 @@ __device__ __forceinline__ void drain_tile(Ctl8* ctl, const Int8Args& a, uint32_
                                            int c0, int m0, int nt, float* xbuf, int warp, int lane) {
     using Y = Elem<DT>;
     const int q = warp & 3, hw = warp >> 2, n = c0 + q * 32 + lane;
-    float ws = n < a.N ? __ldg(a.ws + n) : 0.0f;
+    float ws = n < a.N ? a.ws[n] : 0.0f;
     const int cols = min(nt, a.M - m0);
-    float xl = lane < cols - 32 * hw ? __ldg(a.xs + m0 + 32 * hw + lane) : 0.0f;
+    float xl = lane < cols - 32 * hw ? a.xs[m0 + 32 * hw + lane] : 0.0f;
     // every lane waits; the warp goes on together (the TMEM loads are warp-wide)
     const bool ok = __all_sync(0xffffffffu, wait8(ctl, bar, parity));
     fence_after8();
@@ -354,7 +365,7 @@ __device__ __forceinline__ void drain_tile(Ctl8* ctl, const Int8Args& a, uint32_
         __syncwarp();
         xbuf[lane] = xl;
         if (ok) tmem_ld8(tacc + (uint32_t)j, v);
-        xl = lane < cols - (j + 64) ? __ldg(a.xs + m0 + j + 64 + lane) : 0.0f;
+        xl = lane < cols - (j + 64) ? a.xs[m0 + j + 64 + lane] : 0.0f;
         __syncwarp();
         typename Y::T* y = static_cast<typename Y::T*>(a.y) + (int64_t)(m0 + j) * ldy + n;
         const bool whole = j + 32 <= cols && c0 + kTileCh <= a.N;
@@ -544,7 +555,7 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
             const int per = kTileCh >> lg, parts = 1 << lg;
             const int ch = threadIdx.x & (per - 1), n = c0 + rank * per + ch;
             const uint32_t pitch = 4u * (uint32_t)(nt + 4);
-            float ws = n < a.N ? __ldg(a.ws + n) : 0.0f;
+            float ws = n < a.N ? a.ws[n] : 0.0f;
             for (int r = 0; r < parts; ++r)
                 if (ctl->lost[r]) ws = __int_as_float(0x7fc00000);
             const int cols = min(nt, a.M - m0);
@@ -553,7 +564,7 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
             for (int j = 4 * (int)(threadIdx.x >> (7 - lg)); j < cols; j += 4 * ((kDrainWarps * 32) >> (7 - lg))) {
                 float xs[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xs[i] = j + i < cols ? __ldg(a.xs + m0 + j + i) : 0.0f;
+                for (int i = 0; i < 4; ++i) xs[i] = j + i < cols ? a.xs[m0 + j + i] : 0.0f;
                 int4 v = red[j / 4];
                 for (int r = 1; r < parts; ++r) {
                     const int4 o = red[(uint32_t)r * part_step + j / 4];
@@ -614,7 +625,6 @@ template <int DT, int KPER>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 int8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                  const __grid_constant__ Int8Args a, const __grid_constant__ MmaPlan p) {
-    using Y = Elem<DT>;
     extern __shared__ __align__(1024) unsigned char dsm[];
     const uint32_t raw = s32(dsm);
     const uint32_t base = (raw + 1023u) & ~1023u;

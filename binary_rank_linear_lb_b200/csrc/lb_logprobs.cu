@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
 
     auto load = [&](int j) {
         const int i = j * VE - shift;
-        if (i >= 0 && i + VE <= a.vocab && j < p1) return __ldg(reinterpret_cast<const uint4*>(x + i));
+        if (i >= 0 && i + VE <= a.vocab && j < p1) return *reinterpret_cast<const uint4*>(x + i);
         const float none = -INFINITY;
         uint4 u;
         T* e = reinterpret_cast<T*>(&u);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
         k += batches * kBatch;
         uint4 raw[kBatch];                         // the next batch is requested before one is taken
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) raw[b] = __ldg(p + b * kLpThreads);
+        for (int b = 0; b < kBatch; ++b) raw[b] = p[b * kLpThreads];
         while (true) {
             F2 v[8];
 #pragma unroll
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
             p += kBatch * kLpThreads;
             if (--batches > 0)
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) raw[b] = __ldg(p + b * kLpThreads);
+                for (int b = 0; b < kBatch; ++b) raw[b] = p[b * kLpThreads];
             st.take(v);
             if (batches == 0) break;
         }

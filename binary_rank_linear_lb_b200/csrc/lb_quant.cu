@@ -155,14 +155,14 @@ __device__ __forceinline__ void load_weights(const QuantArgs& a, int i, F2 (&v)[
         if (a.weight_type == LB_F32) {
 #pragma unroll
             for (int j = 0; j < VE; j += 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + i + j));
+                const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + i + j);
                 v[j / 2] = f2(f.x, f.y);
                 v[j / 2 + 1] = f2(f.z, f.w);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < VE; j += 4) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.weight) + i + j));
+                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.weight) + i + j);
                 const uint32_t h[2] = {u.x, u.y};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
             raw[c] = Piece<DT>::pack(xv);
             store_piece<DT, ALIGNED>(sum, at(c), a.cols, raw[c]);
         }
+        __syncwarp();                              // (a lane may have stored part of its neighbour's piece)
     }
     // v = s w, the sum of s^2 and the largest |v|.  (Without a norm v is the row
     // itself and is unpacked again for the codes, which frees registers.)

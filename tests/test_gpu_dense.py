@@ -147,8 +147,8 @@ def test_rmsnorm_quantize(rows, cols, dtype, wdtype):
     check_codes(q, s, dense.rmsnorm_quantize(f64(total), wn, 1e-6), "residual")
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("cols", [640, 8192, 34567])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("cols", [5, 333, 640, 1027, 5001, 8192, 12345, 34567])
 @pytest.mark.parametrize("into", ["x", "residual"])
 def test_rmsnorm_quantize_in_place(dtype, cols, into):
     x, r, w = normal((5, cols), 31, dtype), normal((5, cols), 32, dtype), normal((cols,), 33, F16)
@@ -161,12 +161,21 @@ def test_rmsnorm_quantize_in_place(dtype, cols, into):
 
 
 @pytest.mark.parametrize("dtype", [F16, F32])
-def test_rmsnorm_quantize_pitches(dtype):
-    x, r = in_pitch(normal((6, 777), 41, dtype), 779, 1), in_pitch(normal((6, 777), 42, dtype), 800)
-    out = in_pitch(torch.zeros((6, 777), device="cuda", dtype=dtype), 785, 5)
-    q, s, total = lb.rmsnorm_quantize(x, normal((778,), 43, F16)[1:], r, sum_out=out)
-    assert torch.equal(total, (x.double() + r.double()).to(dtype))
-    check_codes(q, s, dense.rmsnorm_quantize(f64(total), f64(normal((778,), 43, F16)[1:])), "pitch")
+@pytest.mark.parametrize("cols", [7, 200, 777, 2500, 9001])
+@pytest.mark.parametrize("lead", range(8))
+def test_rmsnorm_quantize_pitches(dtype, cols, lead):
+    """Three matrices off 16 bytes by different amounts; nothing beside them is written."""
+    x = in_pitch(normal((6, cols), 41, dtype), cols + 2, lead)
+    r = in_pitch(normal((6, cols), 42, dtype), cols + 23, 3)
+    buf = torch.full((6 * (cols + 9) + 8,), 3.5, device="cuda", dtype=dtype)
+    out = buf[5 * lead % 8:][:6 * (cols + 9)].view(6, cols + 9)[:, :cols]
+    w = normal((cols + 1,), 43, F16)[1:]
+    q, s, total = lb.rmsnorm_quantize(x, w, r, sum_out=out)
+    want = (x.double() + r.double()).to(dtype)
+    assert torch.equal(total, want)
+    check_codes(q, s, dense.rmsnorm_quantize(f64(want), f64(w)), "pitch")
+    out.fill_(3.5)
+    assert (buf == 3.5).all()
 
 
 def test_rmsnorm_of_values_whose_squares_leave_fp32():
@@ -410,6 +419,40 @@ def test_side_stream_and_stream_argument(M):
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("M", [1, 3, 24, 200])
+def test_calls_back_to_back_on_reused_buffers(M):
+    """Each call may start while the one before it runs, and reads what that one writes:
+    a long run without a wait, every buffer reused, gives what waited-for calls give."""
+    n, k, steps = 4099, 776, 24
+    xs = [normal((M, k), 70 + i, BF16) for i in range(steps)]
+    w = normal((k,), 3, F16)
+    wq, ws = lb.quantize_rows(normal((n, k), 4, F16))
+    t = random_tokens(M, n, 5)
+
+    def run(wait):
+        r = normal((M, k), 1, BF16)
+        q, s = pitched(codes(M, k, 2)), torch.empty(M, device="cuda")
+        y = torch.empty((M, n), device="cuda")
+        out = []
+        for x in xs:
+            lb.rmsnorm_quantize(x, w, r, sum_out=r, q=q, scale=s)
+            if wait:
+                torch.cuda.synchronize()
+            lb.linear_int8(q, s, wq, ws, y=y)
+            if wait:
+                torch.cuda.synchronize()
+            lp = lb.token_logprobs(y, t, 3)
+            q2, s2 = lb.quantize_rows(y)
+            if wait:
+                torch.cuda.synchronize()
+            out.append((r.clone(), q.clone(), y.clone(), *lp, q2, s2))
+        torch.cuda.synchronize()
+        return out
+
+    for a, b in zip(run(True), run(False)):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
 @pytest.mark.parametrize("M", [1, 24, 200])
 def test_two_captured_graphs_replayed_together(M):
     """The calls share no scratch: two graphs on two streams, with new inputs, give what
@@ -494,6 +537,8 @@ def test_refusals_on_the_gpu():
         with pytest.raises(lb.LbError):
             call()
     for call in (lambda: lb.linear_int8(q, s, q, s.cpu()), lambda: lb.rmsnorm_quantize(x, residual=x.cpu()),
-                 lambda: lb.token_logprobs(x, torch.zeros(4, dtype=torch.int64))):
+                 lambda: lb.token_logprobs(x, torch.zeros(4, dtype=torch.int64)),
+                 lambda: lb.linear_int8(q, s, q, s.cpu(), stream=torch.cuda.Stream()),
+                 lambda: lb.token_logprobs(x.cpu(), stream=torch.cuda.Stream())):
         with pytest.raises(ValueError):
             call()
