@@ -334,8 +334,9 @@ lb_status lb_rmsnorm_quantize(const void *x, lb_dtype x_dtype, int64_t rows, int
  *   y      : device M x out of y_dtype (LB_F32, LB_F16 or LB_BF16), pitch ldy, written
  * The sum is exact; (sum rounded to fp32) * xs * ws is rounded at each product
  * and then to y_dtype.  -128 is an ordinary code.  A device-side wait that gives
- * up (about 2 s) leaves NaN in the outputs it held up.  The fast kernels read xq and wq in 16-byte
- * pieces (pointers and pitches multiples of 16); other calls run a slower one.
+ * up (about 2 s) leaves NaN in the outputs it held up.  The fast kernels read xq
+ * and wq in 16-byte pieces (pointers and pitches multiples of 16); other calls
+ * run one that is tens of times slower for many tokens.
  * Errors: LB_ERR_INVALID_ARG (null pointer, M, in or out <= 0, M or out > 2^24,
  * M * out > 2^40, in > 131071 (the sum has to fit 32 bits), a pitch below its
  * columns or above 2^32, bad dtype), LB_ERR_ALIGNMENT, LB_ERR_UNSUPPORTED, LB_ERR_CUDA.
