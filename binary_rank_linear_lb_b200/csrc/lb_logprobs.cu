@@ -28,13 +28,11 @@
 namespace lb {
 namespace {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kSplitThreads = 256;           // of each CTA of a split row
 constexpr int kMaxTop = 32;
-constexpr int kGroups = 64;                  // groups of four threads
+constexpr int kGroups = 64;                  // groups of threads whose maxima bound the alternatives
 constexpr int kCandidates = 1024;            // logits >= T kept at most
 constexpr int kLpCluster = 8;
-static_assert(kLpCluster / 2 <= kLpWarps - 1, "a warp merges two lists, the last folds the sums");
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // t below this is as good as -inf (2^t is 0), and unlike it can be multiplied by 0.
@@ -167,17 +165,19 @@ __device__ __forceinline__ void cluster_sync() {
 // A CTA per row, or `parts` CTAs (a cluster).  A row is read as the 16-byte
 // pieces of memory that it touches; the first and the last may lie partly
 // outside it and are read element by element.
-template <int DT, bool SPLIT>
+template <int DT, bool SPLIT, int kLpThreads>
 __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_constant__ LogprobArgs a, int parts) {
     using X = Elem<DT>;
     using T = typename X::T;
-    constexpr int VE = Piece<DT>::VE;
+    constexpr int VE = Piece<DT>::VE, kLpWarps = kLpThreads / 32;
+    static_assert(!SPLIT || kLpCluster / 2 <= kLpWarps - 1, "a warp merges two lists, the last folds the sums");
     constexpr int kBatch = 16 / VE;                // pieces of a batch: 16 logits
     __shared__ float fred[2][kLpWarps];
     __shared__ __align__(8) uint32_t group[kGroups];
     __shared__ int n_cand;
     __shared__ __align__(16) unsigned long long cand[kCandidates];
     __shared__ LpPart part;
+    constexpr int kGroup = kLpThreads / kGroups;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = SPLIT ? (int)(blockIdx.x % parts) : 0;
     const int64_t row = SPLIT ? blockIdx.x / parts : blockIdx.x;
@@ -266,10 +266,11 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
     const bool some = p0 + (int)threadIdx.x < p1;            // this thread holds logits
     const uint32_t key = some ? order_key(st.m) : 0u;
     {
-        // maxima of four threads each, which bound the alternatives, and the row's
-        uint32_t g = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
-        g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
-        if ((lane & 3) == 0) group[threadIdx.x / 4] = g;
+        // maxima of a few threads each, which bound the alternatives, and the row's
+        uint32_t g = key;
+#pragma unroll
+        for (int o = 1; o < kGroup; o *= 2) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if (lane % kGroup == 0) group[threadIdx.x / kGroup] = g;
     }
     const bool nan = __syncthreads_or(st.nan) != 0;
     const uint2 mine2 = *reinterpret_cast<const uint2*>(&group[2 * lane]);   // two groups a lane
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
             // top * 5 / 4 + 1 maxima above it will do.
             uint32_t T0 = 0;
             bool tied = false;                     // most groups share the lowest maximum
-            const int full = ((held < kLpThreads ? held : kLpThreads) + 3) / 4;   // groups with logits
+            const int full = ((held < kLpThreads ? held : kLpThreads) + kGroup - 1) / kGroup;   // groups with logits
             if (full >= a.top) {
                 const uint32_t a0 = mine2.x ? mine2.x : 0xffffffffu, a1 = mine2.y ? mine2.y : 0xffffffffu;
                 const uint32_t lo = T0 = __reduce_min_sync(0xffffffffu, min(a0, a1));
@@ -536,8 +537,23 @@ int row_parts(int64_t rows, int64_t vocab, int sms) {
 template <int DT>
 cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, int sms, cudaStream_t s) {
     const int parts = row_parts(rows, a.vocab, sms);
-    if (parts == 1) return launch_dense(logprobs_kernel<DT, false>, (unsigned)rows, kLpThreads, 0, 1, s, a, 1);
-    return launch_dense(logprobs_kernel<DT, true>, (unsigned)(rows * parts), kLpThreads, 0, (unsigned)parts, s, a, parts);
+    if (parts > 1)
+        return launch_dense(logprobs_kernel<DT, true, kSplitThreads>, (unsigned)(rows * parts), kSplitThreads, 0,
+                            (unsigned)parts, s, a, parts);
+    // Threads of a row.  Rows that come in many waves and are short spend their time in
+    // the folds: fewer threads a row put more rows on an SM, whose folds then overlap
+    // others' loads.  Measured (us, 64 / 128 / 256 threads, top 5): 4096 x 4099 fp32 [22.6]
+    // 28.4 39.0, 2500 x 5430 bf16 [15.0] 21.7 26.2; 4096 x 16000 fp32 58.9 [54.9] 61.5,
+    // 600 x 2000 bf16 8.4 [6.0] 7.7, 4096 x 32000 bf16 [68] against 77; 1000 x 32000 fp32
+    // 41.8 28.9 [27.8], 4096 x 32000 fp32 [96.9] against 99.7.
+    const int64_t bytes = (int64_t)a.vocab * (int64_t)sizeof(typename Elem<DT>::T);
+    const unsigned threads = rows >= 16 * (int64_t)sms && bytes <= 24 * 1024  ? 64
+                             : rows >= 4 * (int64_t)sms && bytes <= 64 * 1024 ? 128
+                                                                              : 256;
+    auto kernel = threads == 64    ? logprobs_kernel<DT, false, 64>
+                  : threads == 128 ? logprobs_kernel<DT, false, 128>
+                                   : logprobs_kernel<DT, false, 256>;
+    return launch_dense(kernel, (unsigned)rows, threads, 0, 1, s, a, 1);
 }
 
 }  // namespace
