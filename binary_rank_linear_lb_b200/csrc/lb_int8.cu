@@ -77,21 +77,20 @@ __global__ void __launch_bounds__(256) int8_general_kernel(const __grid_constant
     }
 }
 
-// ------------------------------------------------------------ few tokens
-// One or two tokens, and up to four over a small weight: the weights stream past
-// once and __dp4a keeps up (M products of four per weight word, against 64 a clock
-// and SM).  A warp takes four channels and, with few channels, a block's warps
-// share their K (`parts`), so that every SM has some 100 KB of weights in flight;
-// a lane holds 16 bytes of every row, 512 contiguous bytes a warp.  xq comes from L1.
+// ------------------------------------------------------------ one token
+// The weights stream past once and __dp4a keeps up.  A warp takes two channels and,
+// with few channels, a block's warps share their K (`parts`), so that every SM has
+// some 100 KB of weights in flight; a lane holds 16 bytes of every row, 512
+// contiguous bytes a warp, four such chunks requested together.  xq comes from L1.
 //
-// Against the tensor cores (us): 4096 -> 32000, one token 22.9 / 23.1, two 24.9 /
-// 24.7, four 29.4 / 24.7; 4096 -> 4096, one 5.2 / 6.1, four 6.8 / 6.1 (the set-up
-// of barriers, TMEM and tensor maps); 1024 -> 1024, one 2.4 / 4.8, four 2.6 / 4.8.
-// What bounds it: HBM, 5.8 TB/s (90% of the copy rate) at one token, 4096 -> 32000.
-constexpr int kFewThreads = 256;
-constexpr int kFewWarps = kFewThreads / 32;
-constexpr int kFewCh = 4;                          // channels of a warp
-constexpr int kFewTok = 4;                         // tokens at most
+// Against the tensor cores (us, weights from HBM): 4096 -> 32000 [21.4] 22.2, 8192
+// -> 28672 [38.3] 38.9, 4096 -> 4096 [4.8] 6.8, 1024 -> 1024 [2.2] 3.6 (no barriers,
+// TMEM and tensor maps to set up).  From two tokens on the products catch up with
+// the loads: 4096 -> 32000 30.6 against [22.4], 4096 -> 4096 8.6 against [6.8].
+// What bounds it: HBM, 6.1 to 6.3 TB/s (95 to 99% of the copy rate) at 4096 -> 32000.
+constexpr int kOneThreads = 256;
+constexpr int kOneWarps = kOneThreads / 32;
+constexpr int kOneCh = 2;                          // channels of a warp
 
 __device__ __forceinline__ int dot16(int4 a, int4 b, int acc) {
     acc = __dp4a(a.x, b.x, acc);
@@ -106,86 +105,69 @@ __device__ __forceinline__ int4 ld_once(const int8_t* p) {
     return v;
 }
 
-template <int DT, int MT>
-__global__ void __launch_bounds__(kFewThreads) int8_few_kernel(const __grid_constant__ Int8Args a, int parts) {
+template <int DT>
+__global__ void __launch_bounds__(kOneThreads) int8_one_kernel(const __grid_constant__ Int8Args a, int parts) {
     using Y = Elem<DT>;
-    __shared__ int part_sums[kFewWarps][kFewCh * MT];
+    __shared__ int part_sums[kOneWarps][kOneCh];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = warp % parts;
-    const int64_t n0 = ((int64_t)blockIdx.x * (kFewWarps / parts) + warp / parts) * kFewCh;
+    const int64_t n0 = ((int64_t)blockIdx.x * (kOneWarps / parts) + warp / parts) * kOneCh;
     const int chunks = a.K / 16;                   // whole 16-byte chunks of a row
     const int c0 = (int)((int64_t)chunks * part / parts), c1 = (int)((int64_t)chunks * (part + 1) / parts);
-    int acc[kFewCh][MT] = {};
-    const int8_t* w[kFewCh];
-    const int8_t* x[MT];
+    const int4* x = reinterpret_cast<const int4*>(a.x);
+    const int8_t* w[kOneCh];
 #pragma unroll
-    for (int i = 0; i < kFewCh; ++i) w[i] = a.w + (n0 + i < a.N ? n0 + i : a.N - 1) * a.ldw;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = a.x + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
+    for (int i = 0; i < kOneCh; ++i) w[i] = a.w + (n0 + i < a.N ? n0 + i : a.N - 1) * a.ldw;
     grid_trigger();
     grid_wait();
-    constexpr int kAhead = 2;                      // chunks requested together
+    int acc[kOneCh] = {};
+    constexpr int kAhead = 4;                      // chunks requested together
     int c = c0 + lane;
     for (; c + 32 * (kAhead - 1) < c1; c += 32 * kAhead) {
-        int4 wv[kAhead][kFewCh];
+        int4 wv[kAhead][kOneCh];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-            for (int i = 0; i < kFewCh; ++i) wv[u][i] = ld_once(w[i] + 16 * (int64_t)(c + 32 * u));
+            for (int i = 0; i < kOneCh; ++i) wv[u][i] = ld_once(w[i] + 16 * (int64_t)(c + 32 * u));
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+        for (int u = 0; u < kAhead; ++u) {
+            const int4 xv = x[c + 32 * u];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int4 xv = reinterpret_cast<const int4*>(x[m])[c + 32 * u];
-#pragma unroll
-                for (int i = 0; i < kFewCh; ++i) acc[i][m] = dot16(wv[u][i], xv, acc[i][m]);
-            }
-    }
-    for (; c < c1; c += 32)
-#pragma unroll
-        for (int i = 0; i < kFewCh; ++i) {
-            const int4 wv = ld_once(w[i] + 16 * (int64_t)c);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[i][m] = dot16(wv, reinterpret_cast<const int4*>(x[m])[c], acc[i][m]);
+            for (int i = 0; i < kOneCh; ++i) acc[i] = dot16(wv[u][i], xv, acc[i]);
         }
-    if (part == parts - 1 && lane < a.K - 16 * chunks)           // the last bytes, one a lane
+    }
+    for (; c < c1; c += 32) {
+        const int4 xv = x[c];
 #pragma unroll
-        for (int i = 0; i < kFewCh; ++i)
+        for (int i = 0; i < kOneCh; ++i) acc[i] = dot16(ld_once(w[i] + 16 * (int64_t)c), xv, acc[i]);
+    }
+    if (part == parts - 1 && lane < a.K - 16 * chunks)             // the last bytes, one a lane
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-                acc[i][m] += (int)w[i][16 * chunks + lane] * (int)x[m][16 * chunks + lane];
+        for (int i = 0; i < kOneCh; ++i) acc[i] += (int)w[i][16 * chunks + lane] * (int)a.x[16 * chunks + lane];
 #pragma unroll
-    for (int i = 0; i < kFewCh; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[i][m] = __reduce_add_sync(0xffffffffu, acc[i][m]);
-    // lane (i, m) of the group's first warp stores channel n0 + i of token m
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < kFewCh; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) if (lane == m * kFewCh + i) sum = acc[i][m];
+    for (int i = 0; i < kOneCh; ++i) acc[i] = __reduce_add_sync(0xffffffffu, acc[i]);
+    // lane i of the group's first warp stores channel n0 + i
+    int sum = lane == 0 ? acc[0] : acc[1];
+    static_assert(kOneCh == 2, "a lane per channel");
     if (parts > 1) {
-        if (lane < kFewCh * MT) part_sums[warp][lane] = sum;
+        if (lane < kOneCh) part_sums[warp][lane] = sum;
         __syncthreads();
         if (part != 0) return;
-        if (lane < kFewCh * MT)
+        if (lane < kOneCh)
             for (int p = 1; p < parts; ++p) sum += part_sums[warp + p][lane];
     }
-    const int m = lane / kFewCh;
-    const int64_t n = n0 + lane % kFewCh;
-    if (lane < kFewCh * MT && m < a.M && n < a.N)
-        static_cast<typename Y::T*>(a.y)[(int64_t)m * a.ldy + n] = Y::put((float)sum * a.xs[m] * a.ws[n]);
+    const int64_t n = n0 + lane;
+    if (lane < kOneCh && n < a.N) static_cast<typename Y::T*>(a.y)[n] = Y::put((float)sum * a.xs[0] * a.ws[n]);
 }
 
 template <int DT>
-cudaError_t launch_few(const Int8Args& a, int sms, cudaStream_t s) {
-    const int64_t groups = ((int64_t)a.N + kFewCh - 1) / kFewCh;
+cudaError_t launch_one(const Int8Args& a, int sms, cudaStream_t s) {
+    const int64_t groups = ((int64_t)a.N + kOneCh - 1) / kOneCh;
     int parts = 1;
-    while (parts < kFewWarps && groups * parts < (int64_t)sms * 24 && a.K / (parts * 2) >= 1024) parts *= 2;
-    const int per_block = kFewWarps / parts;
-    const unsigned blocks = (unsigned)((groups + per_block - 1) / per_block);
-    auto kernel = a.M == 1 ? int8_few_kernel<DT, 1> : a.M == 2 ? int8_few_kernel<DT, 2> : int8_few_kernel<DT, 4>;
-    return launch_dense(kernel, blocks, kFewThreads, 0, 1, s, a, parts);
+    while (parts < kOneWarps && groups * parts < (int64_t)sms * 24 && a.K / (parts * 2) >= 512) parts *= 2;
+    const int per_block = kOneWarps / parts;
+    return launch_dense(int8_one_kernel<DT>, (unsigned)((groups + per_block - 1) / per_block), kOneThreads, 0, 1, s, a,
+                        parts);
 }
 
 // ------------------------------------------------------------ tensor cores
@@ -897,8 +879,8 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const Int8Args a = {xq, wq, xs, ws, y, ldx, ldw, ldy, (int)M, (int)out, (int)in};
     if (mma_ok(a)) {
-        if (M <= kFewTok && (M <= 2 || in * out < (1 << 25))) {
-            const cudaError_t e = with_dtype(y_dtype, [&](auto d) { return launch_few<d.value>(a, sms, s); });
+        if (M == 1) {
+            const cudaError_t e = with_dtype(y_dtype, [&](auto d) { return launch_one<d.value>(a, sms, s); });
             return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
         }
         const MmaPlan p = mma_plan(M, out, in, sms);
