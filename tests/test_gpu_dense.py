@@ -484,6 +484,46 @@ def test_two_captured_graphs_replayed_together(M):
             assert all(torch.equal(a, b) for a, b in zip(outs[i], chain(*sets[i])))
 
 
+@pytest.mark.parametrize("M", [1, 17, 150])
+def test_captured_among_copies_and_joined_streams(M):
+    """In a graph, a call that follows a copy or a memset and one that joins two streams
+    wait for all of them."""
+    k, n = 528, 640
+    src, wsrc = normal((M, k), 1, F16), normal((n, k), 2, F16)
+    buf, wbuf, junk = torch.empty_like(src), torch.empty_like(wsrc), torch.empty(1 << 20, device="cuda")
+    t = random_tokens(M, n, 3)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def body(fork):
+        buf.copy_(src)
+        q, s = lb.quantize_rows(buf)
+        if fork:
+            side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side) if fork else torch.cuda.stream(torch.cuda.current_stream()):
+            wbuf.copy_(wsrc)
+            wq, ws = lb.quantize_rows(wbuf)
+        if fork:
+            torch.cuda.current_stream().wait_stream(side)
+        y = lb.linear_int8(q, s, wq, ws)
+        junk.zero_()
+        r = lb.token_logprobs(y, t, 3)
+        y2 = y * 2
+        return (q, s, wq, ws, y, *r, y2, *lb.quantize_rows(y2))
+
+    body(False)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        out = body(True)
+    for rep in range(5):
+        src.copy_(normal((M, k), 10 + rep, F16))
+        wsrc.copy_(normal((n, k), 20 + rep, F16))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, body(False)))
+
+
 # -------------------------------------------------------------- a run of them together
 @pytest.mark.parametrize("norm_weight", [True, False])
 def test_stack_and_head_end_to_end(norm_weight):
