@@ -21,49 +21,96 @@ struct Int8Args {
     int M, N, K;
 };
 
-// General kernel: any pitch and alignment.  64 x 64 outputs per block, 64
-// columns of K at a time through shared memory (bytes loaded one by one, zero
-// past the edges), four rows by four columns per thread with __dp4a.
+// General kernel: any pitch and alignment.  16 R tokens x 64 channels per block, 64
+// columns of K at a time through two stages of shared memory, R tokens by four
+// channels per thread with __dp4a.
+//
+// What bounds it: latency of a stage's loads with few blocks, reads of shared memory
+// with many; two words are loaded for each one used.  4097 -> 32000, one token: 140 us
+// (0.9 TB/s; rows on 16 bytes 21); 4097 -> 4096, 64 tokens 98 us, 512 tokens 256 us
+// (67 TOP/s).  Byte by byte these were 500, 216 and 485 us.
 constexpr int kGenTile = 64;
 constexpr int kGenPitch = 17;                // words of a staged row (16 used), odd: no bank conflicts
 
-template <int DT>
+// Codes k .. k + 3 of a row of K that starts anywhere, 0 past its end, from the two
+// aligned words that hold them.  A word is read only if it holds a code of the row.
+__device__ __forceinline__ int codes_at(const int8_t* row, int k, int K) {
+    if (k >= K) return 0;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + k);
+    const int off = (int)(at & 3);
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(at - off);
+    const uint32_t lo = p[0], hi = off > 0 && k + 4 - off < K ? p[1] : 0;
+    const uint32_t v = __funnelshift_r(lo, hi, 8 * off);
+    return (int)(K - k < 4 ? v & ((1u << 8 * (K - k)) - 1) : v);
+}
+
+template <int DT, int R>
 __global__ void __launch_bounds__(256) int8_general_kernel(const __grid_constant__ Int8Args a) {
-    __shared__ int xt[kGenTile * kGenPitch], wt[kGenTile * kGenPitch];
-    const int n_m = (a.M + kGenTile - 1) / kGenTile;
-    const int m0 = (int)(blockIdx.x % n_m) * kGenTile, n0 = (int)(blockIdx.x / n_m) * kGenTile;
+    __shared__ int xt[2][16 * R * kGenPitch], wt[2][kGenTile * kGenPitch];
+    const int n_m = (a.M + 16 * R - 1) / (16 * R);
+    const int m0 = (int)(blockIdx.x % n_m) * (16 * R), n0 = (int)(blockIdx.x / n_m) * kGenTile;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    // Rows past the last are the last again: what they give is not stored.
+    const int8_t* row[R + 4];
+    int off[R + 4];
+#pragma unroll
+    for (int i = 0; i < R + 4; ++i) {
+        const int m = m0 + ty + 16 * i, n = n0 + ty + 16 * (i - R);
+        row[i] = i < R ? a.x + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx : a.w + (int64_t)(n < a.N ? n : a.N - 1) * a.ldw;
+        off[i] = (int)(reinterpret_cast<uintptr_t>(row[i]) & 3);
+    }
+    // Words tx of the next stage's rows.  While a code follows the stage's 64, both
+    // aligned words of each hold codes of the row: all are requested without a
+    // condition, which would make each load wait for the one before it.
+    uint32_t lo[R + 4], hi[R + 4];
+    const auto fetch = [&](int k0) {
+        const int k = k0 + 4 * tx;
+        if (k0 + 64 < a.K) {
+#pragma unroll
+            for (int i = 0; i < R + 4; ++i) {
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(row[i] + k - off[i]);
+                lo[i] = p[0];
+                hi[i] = p[1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R + 4; ++i) {
+                const uint64_t v = (uint64_t)(uint32_t)codes_at(row[i], k, a.K) << 8 * off[i];
+                lo[i] = (uint32_t)v;
+                hi[i] = (uint32_t)(v >> 32);
+            }
+        }
+    };
     grid_trigger();
     grid_wait();
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 64) {
-        for (int i = threadIdx.x; i < kGenTile * 64; i += 256) {
-            const int r = i >> 6, c = i & 63, k = k0 + c;
-            int8_t xv = 0, wv = 0;
-            if (k < a.K && m0 + r < a.M) xv = a.x[(int64_t)(m0 + r) * a.ldx + k];
-            if (k < a.K && n0 + r < a.N) wv = a.w[(int64_t)(n0 + r) * a.ldw + k];
-            reinterpret_cast<int8_t*>(xt + r * kGenPitch)[c] = xv;
-            reinterpret_cast<int8_t*>(wt + r * kGenPitch)[c] = wv;
+    int acc[R][4] = {};
+    fetch(0);
+    for (int k0 = 0, stage = 0; k0 < a.K; k0 += 64, stage ^= 1) {
+#pragma unroll
+        for (int i = 0; i < R + 4; ++i) {
+            const int v = (int)__funnelshift_r(lo[i], hi[i], 8 * off[i]);
+            if (i < R) xt[stage][(ty + 16 * i) * kGenPitch + tx] = v;
+            else wt[stage][(ty + 16 * (i - R)) * kGenPitch + tx] = v;
         }
+        // Two stages: whoever is past this has read the other stage to its end.
         __syncthreads();
+        if (k0 + 64 < a.K) fetch(k0 + 64);
 #pragma unroll 4
         for (int kk = 0; kk < 16; ++kk) {
-            int xv[4], wv[4];
+            int xv[R], wv[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                xv[i] = xt[(ty + 16 * i) * kGenPitch + kk];
-                wv[i] = wt[(tx + 16 * i) * kGenPitch + kk];
-            }
+            for (int i = 0; i < R; ++i) xv[i] = xt[stage][(ty + 16 * i) * kGenPitch + kk];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) wv[i] = wt[stage][(tx + 16 * i) * kGenPitch + kk];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(xv[i], wv[j], acc[i][j]);
         }
-        __syncthreads();
     }
     using Y = Elem<DT>;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         const int m = m0 + ty + 16 * i;
         if (m >= a.M) continue;
         const float xs = a.xs[m];
@@ -75,6 +122,15 @@ __global__ void __launch_bounds__(256) int8_general_kernel(const __grid_constant
                     Y::put((float)acc[i][j] * xs * a.ws[n]);
         }
     }
+}
+
+// Tokens of a block's tile, 16 / 32 / 64, in us: 4097 -> 32000, 16 tokens [143] 170 245,
+// 17 tokens 238 [170] 245, 32 tokens 240 [173] 248, 48 tokens 369 292 [250]; 4097 ->
+// 4096, 32 tokens 103 [55] 106, 512 tokens 465 293 [256].
+template <int DT, int R>
+cudaError_t launch_general(const Int8Args& a, cudaStream_t s) {
+    const int64_t blocks = ((int64_t)a.M + 16 * R - 1) / (16 * R) * (((int64_t)a.N + kGenTile - 1) / kGenTile);
+    return launch_dense(int8_general_kernel<DT, R>, (unsigned)blocks, 256, 0, 1, s, a);
 }
 
 // ------------------------------------------------------------ one token
@@ -901,9 +957,10 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
         });
         return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
     }
-    const int64_t blocks = ((M + kGenTile - 1) / kGenTile) * ((out + kGenTile - 1) / kGenTile);
     const cudaError_t e = with_dtype(y_dtype, [&](auto d) {
-        return launch_dense(int8_general_kernel<d.value>, (unsigned)blocks, 256, 0, 1, s, a);
+        return M <= 16   ? launch_general<d.value, 1>(a, s)
+               : M <= 32 ? launch_general<d.value, 2>(a, s)
+                         : launch_general<d.value, 4>(a, s);
     });
     return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
 }

@@ -251,6 +251,17 @@ def test_linear_int8_pitches(M, ldx, leadx, ldw, leadw):
     assert (edge == 5.0).all()                        # nothing around y was written
 
 
+@pytest.mark.parametrize("M", [1, 15, 16, 17, 64, 65])
+@pytest.mark.parametrize("lead", [0, 1, 2, 3])
+def test_linear_int8_off_words(M, lead):
+    """Rows that start and end anywhere in a word, around a word's and a stage's end; the
+    codes beside them are 77."""
+    for k in (1, 2, 3, 4, 5, 63, 64, 65, 66, 127, 128, 129, 131):
+        xq, wq = in_pitch(codes(M, k, k), k + 5, (lead + 1) % 4), in_pitch(codes(67, k, k + 1), k + 6, lead)
+        xs, ws = scales(M, 5), scales(67, 6)
+        check_linear(lb.linear_int8(xq, xs, wq, ws), xq, xs, wq, ws, (M, k, lead))
+
+
 @pytest.mark.parametrize("M", [1, 4, 16, 130])
 def test_linear_int8_largest_sums(M):
     """in = 131071 rows of -128: sums of 2147467264, the largest there are."""
