@@ -9,7 +9,9 @@
 // batches is rare), in powers of two: t = (x - m) log2 e, S = sum 2^t,
 // A = sum 2^t t.  The threads' triples are folded at the end.  What bounds it:
 // HBM for fp32, the exponentials (16 a clock and SM) and the instructions around
-// them (about 5 an element) close behind for 16-bit logits.
+// them (about 5 an element) close behind for 16-bit logits.  4096 x 32000, top 5: fp32
+// 98 to 103 us, 5.1 to 5.3 TB/s (79 to 83% of the copy rate); bf16 67 us, 3.9 TB/s (55
+// us without alternatives: those cost a second look at some pieces and the ranking).
 //
 // The alternatives need no second pass either: the threads' maxima bound them.
 // If `top` of the maxima of 64 groups of threads are >= T, the alternatives are

@@ -17,7 +17,10 @@
 //
 // What bounds it: HBM.  A row is read once and kept in registers as v between
 // the two halves (peak and mean square, then the codes): rows up to 1024 columns
-// by one warp, up to 32768 by one block; wider ones read memory twice.
+// by one warp, up to 32768 by one block; wider ones read memory twice.  Codes of
+// 32000 x 4096 bf16: 66 to 69 us, 5.7 to 6.0 TB/s (89 to 93% of the copy rate); norm of
+// 4096 x 8192 bf16 with residual and sum: 42 to 44 us, 5.4 to 5.6 TB/s (83 to 87%).
+// Rows off 16 bytes load each piece from two: 100000 x 777 bf16 105 us, x 776 61 us.
 #include <cmath>
 
 #include "lb_dense.cuh"
@@ -421,7 +424,8 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
 }
 
 // Rows of more columns than a block's registers hold: one block per row, in 64
-// bits, the row read twice.
+// bits, the row read twice.  Bound by the 64-bit arithmetic and by loads of one
+// element: 4096 x 40000 fp32 715 to 730 us, 1.1 TB/s (17% of the copy rate).
 template <int DT>
 __global__ void __launch_bounds__(256) quant_wide_kernel(const __grid_constant__ QuantArgs a) {
     using X = Elem<DT>;
