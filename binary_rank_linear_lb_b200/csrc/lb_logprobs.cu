@@ -52,14 +52,16 @@ struct LogprobArgs {
 };
 
 // Order of the alternatives as an unsigned key: larger logit first, NaN before
-// everything, -0 equal to +0.  Key 0 is below every logit.
+// everything, -0 equal to +0.  Key 0 is below every logit; 0xffffffff is left free, so
+// that every entry (entry_of) is below ~0, where the rounds of a maximum start.
+constexpr uint32_t kNanKey = 0xfffffffeu;           // (+inf: 0xff800000)
 __device__ __forceinline__ uint32_t order_key(float v) {
-    if (v != v) return 0xffffffffu;
+    if (v != v) return kNanKey;
     const uint32_t u = __float_as_uint(v + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
-    return k == 0xffffffffu ? NAN : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+    return k == kNanKey ? NAN : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 // Key and index as one number: larger is earlier (equal keys by rising index).
 __device__ __forceinline__ unsigned long long entry_of(uint32_t key, int i) {
