@@ -36,7 +36,8 @@ def sources():
 
 
 def deps():
-    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
+    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) +
+                              glob.glob(os.path.join(CSRC, "*.h"))) + [
         os.path.join(ROOT, "include", "lb.h")]
 
 

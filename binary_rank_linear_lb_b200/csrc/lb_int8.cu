@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "lb_dense.cuh"
+#include "lb_drain.h"
 
 namespace lb {
 namespace {
@@ -380,12 +381,12 @@ __device__ __forceinline__ void st_cluster8(uint32_t addr, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
 }
 
-// Waits for an accumulator and stores it, a warp a quarter of the lanes (lane =
+// Waits for the turn's accumulator and stores it, a warp a quarter of the lanes (lane =
 // channel c0 + 32 (warp & 3) + lane) and every other 32 columns (tokens m0 ..).  The
 // tokens' scales go through a shared buffer of the warp (xbuf, 32 floats) to be read
 // four at a time: a shuffle a column shared the stores' queue.
 template <int DT>
-__device__ __forceinline__ void drain_tile(Ctl8* ctl, const Int8Args& a, uint32_t bar, uint32_t parity, uint32_t tacc,
+__device__ __forceinline__ void drain_tile(DrainTurn& turn, Ctl8* ctl, const Int8Args& a, uint32_t bar, uint32_t tacc,
                                            int c0, int m0, int nt, float* xbuf, int warp, int lane) {
     using Y = Elem<DT>;
     const int q = warp & 3, hw = warp >> 2, n = c0 + q * 32 + lane;
@@ -393,7 +394,8 @@ __device__ __forceinline__ void drain_tile(Ctl8* ctl, const Int8Args& a, uint32_
     const int cols = min(nt, a.M - m0);
     float xl = lane < cols - 32 * hw ? a.xs[m0 + 32 * hw + lane] : 0.0f;
     // every lane waits; the warp goes on together (the TMEM loads are warp-wide)
-    const bool ok = __all_sync(0xffffffffu, wait8(ctl, bar, parity));
+    const bool ok =
+        turn.full([&](uint32_t parity) { return __all_sync(0xffffffffu, wait8(ctl, bar, parity)) != 0; });
     fence_after8();
     if (!ok) ws = __int_as_float(0x7fc00000);      // NaN: the sums are not there
     tacc += (uint32_t)(q * 32) << 16;
@@ -570,14 +572,14 @@ int8_mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant_
             if (!ok && lane < (1 << lg)) st_cluster8(peer_addr8(s32(&ctl->lost[rank]), (uint32_t)lane), 1);
         }
     } else {
-        int tl = 0;
-        for (int t = first; t < n_tiles; t += step, ++tl) {
-            const uint32_t buf = tl & 1;
-            drain_tile<DT>(ctl, a, acc_full + 8u * buf, (tl >> 1) & 1, tmem + buf * (uint32_t)p.acc_cols,
+        DrainTurn turn;
+        for (int t = first; t < n_tiles; t += step, turn.next()) {
+            const uint32_t buf = turn.buf();
+            drain_tile<DT>(turn, ctl, a, acc_full + 8u * buf, tmem + buf * (uint32_t)p.acc_cols,
                            (t / n_tok) * kTileCh, (t % n_tok) * nt, nt, ctl->xbuf[warp], warp, lane);
             fence_before8();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
+            if (turn.alive && lane == 0) mbar_arrive(acc_empty + 8u * buf);
         }
     }
     if constexpr (SPLIT) {
@@ -775,14 +777,14 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
         }
     } else {
         const uint32_t acc_empty0 = peer_addr8(acc_empty, 0);
-        int tl = 0;
-        for (int t = first; t < n_tiles; t += step, ++tl) {
-            const uint32_t buf = tl & 1;
-            drain_tile<DT>(ctl, a, acc_full + 8u * buf, (tl >> 1) & 1, tmem + buf * (uint32_t)p.acc_cols,
+        DrainTurn turn;
+        for (int t = first; t < n_tiles; t += step, turn.next()) {
+            const uint32_t buf = turn.buf();
+            drain_tile<DT>(turn, ctl, a, acc_full + 8u * buf, tmem + buf * (uint32_t)p.acc_cols,
                            (t / n_tok) * 2 * kTileCh + rank * kTileCh, (t % n_tok) * nt, nt, ctl->xbuf[warp], warp, lane);
             fence_before8();
             __syncwarp();
-            if (lane == 0) arrive_peer8(acc_empty0 + 8u * buf);
+            if (turn.alive && lane == 0) arrive_peer8(acc_empty0 + 8u * buf);
         }
     }
     __syncthreads();
