@@ -10,10 +10,10 @@
 // Rounding.  The codes are those of the exact quotient.  It is computed in fp32,
 // where its error (see kBorder) can move it over the border between two codes,
 // so quotients that near a border are computed again in 64 bits, where s_i w_i
-// is exact.  peak is exact too: the fp32 products that share the largest value
-// are compared again in 64 bits (unless no product rounds).  Rows whose peak or
-// mean square leaves fp32's comfortable range, rows of zeros and rows with a
-// NaN or an infinity are computed in 64 bits altogether.
+// is exact (127 s_i w_i not always: above_border).  peak is exact too: the fp32
+// products that share the largest value are compared again in 64 bits (unless no
+// product rounds).  Rows whose peak or mean square leaves fp32's comfortable range,
+// rows of zeros and rows with a NaN or an infinity are computed in 64 bits altogether.
 //
 // What bounds it: HBM.  A row is read once and kept in registers as v between
 // the two halves (peak and mean square, then the codes): rows up to 1024 columns
@@ -208,9 +208,22 @@ __device__ __forceinline__ int code_d(double s, double w, double peak) {
     return __double2int_rn(s * w * 127.0 / peak);
 }
 
+// The code of v where the quotient 127 |v| / peak is within 2^-13 of the border lo + 1/2: lo
+// or lo + 1, ties to even, with v's sign.  For the norm of fp32 rows, as products of two
+// fp32 have up to 48 bits: 127 v can need 55, rounds in code_d, and a tie may be missed.
+// (All other products have 35 bits at most; 127 v is exact, and a quotient that is not on a
+// border is at least 2^-44 from it and off by less than 2^-46.)  Here both sides are
+// compared as they are: 127 |v| = p + e and (lo + 1/2) peak = p + d, where e, the rest of a
+// product, and d, a difference of 42 bits at most, are exact.
+__device__ __forceinline__ int above_border(double v, int lo, double peak) {
+    const double p = 127.0 * fabs(v), e = fma(127.0, fabs(v), -p), d = fma(lo + 0.5, peak, -p);
+    const int k = lo + (e > d || (e == d && (lo & 1)));
+    return v < 0.0 ? -k : k;
+}
+
 // A row in 64 bits, from memory (its sums already written): every thread
 // takes the columns first, first + step, ...
-template <int DT, bool WARP>
+template <int DT, bool WARP, bool EXACT>
 __device__ __noinline__ void quant_row_64(const QuantArgs& a, int64_t row, int first, int step, double* red) {
     using X = Elem<DT>;
     const typename X::T* s = a.residual ? static_cast<const typename X::T*>(a.sum) + row * a.lds
@@ -229,31 +242,56 @@ __device__ __noinline__ void quant_row_64(const QuantArgs& a, int64_t row, int f
     const double size = a.norm ? 1.0 / sqrt(ss / a.cols + (double)a.eps) : 1.0;
     if (first == 0) a.scale[row] = bad ? NAN : peak > 0.0 ? (float)(peak * size / 127.0) : 0.0f;
     int8_t* q = a.q + row * a.ldq;
-    for (int i = first; i < a.cols; i += step)
-        q[i] = bad || !(peak > 0.0)
-                   ? 0
-                   : (int8_t)code_d((double)X::get(s[i]), (double)weight_at(a.weight, a.weight_type, i), peak);
+    if constexpr (EXACT) {
+        if (bad || !(peak > 0.0)) {
+            for (int i = first; i < a.cols; i += step) q[i] = 0;
+            return;
+        }
+        const double inv = 127.0 / peak;
+        for (int i = first; i < a.cols; i += step) {
+            const double v = (double)X::get(s[i]) * (double)weight_at(a.weight, a.weight_type, i);
+            const double quotient = v * inv;       // (off by less than 2^-45)
+            q[i] = (int8_t)__double2int_rn(quotient);
+            if (fabs(quotient - rint(quotient)) > 0.5 - 0x1p-40)
+                q[i] = (int8_t)above_border(v, (int)fabs(quotient), peak);
+        }
+    } else {
+        for (int i = first; i < a.cols; i += step)
+            q[i] = bad || !(peak > 0.0)
+                       ? 0
+                       : (int8_t)code_d((double)X::get(s[i]), (double)weight_at(a.weight, a.weight_type, i), peak);
+    }
 }
 
 // The code of column i again, in 64 bits (rare: a quotient that near a border
 // comes up once in 16,000, and for v = peak / 2).
-template <int DT>
+template <int DT, bool EXACT>
 __device__ __noinline__ void settle_code(const QuantArgs& a, int64_t row, int i, double peak) {
     using X = Elem<DT>;
     const typename X::T* s = a.residual ? static_cast<const typename X::T*>(a.sum) + row * a.lds
                                         : static_cast<const typename X::T*>(a.x) + row * a.ldx;
-    if (i < a.cols)
-        a.q[row * a.ldq + i] =
-            (int8_t)code_d((double)X::get(s[i]), (double)weight_at(a.weight, a.weight_type, i), peak);
+    if constexpr (EXACT) {
+        if (i < a.cols) {                          // (the quotient is within 2^-13 of a border in fp32 too)
+            const double v = (double)X::get(s[i]) * (double)weight_at(a.weight, a.weight_type, i);
+            a.q[row * a.ldq + i] = (int8_t)above_border(v, (int)(127.0f * fabsf((float)v) / (float)peak), peak);
+        }
+    } else {
+        if (i < a.cols)
+            a.q[row * a.ldq + i] =
+                (int8_t)code_d((double)X::get(s[i]), (double)weight_at(a.weight, a.weight_type, i), peak);
+    }
 }
 
 // C pieces of VE elements per thread; a warp per row (8 to a block) or a block
 // per row.  The work is as much in the instructions as in the bytes (a 16-bit
 // element comes and goes with 3 to 7 bytes), so everything runs on pairs and the
 // codes take two pair instructions: v * 127 / peak + kRound holds the code in its
-// low byte, and what it left over says how near the border was.
+// low byte, and what it left over says how near the border was.  (Where a thread holds 32
+// fp32 of a norm off 16 bytes one block an SM is asked for: left to itself the compiler
+// makes room for two by 1.4 KB of spills.)
 template <int DT, int C, bool ALIGNED, bool WARP, int THREADS, bool NORM>
-__global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(THREADS, NORM && !ALIGNED && !WARP && DT == LB_F32 && C == 8 ? 1 : 0)
+quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int VE = Piece<DT>::VE, P = VE / 2;
     __shared__ double red[WARP ? 1 : 32];
@@ -337,7 +375,7 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
     const float peak = __uint_as_float(bits);
     const float ms = ss / (float)a.cols;
     if (!(peak >= kLow && peak <= kHigh) || (NORM && !(ms >= kLow && ms <= kHigh))) {
-        quant_row_64<DT, WARP>(a, row, t, tr, red);
+        quant_row_64<DT, WARP, NORM && DT == LB_F32>(a, row, t, tr, red);
         return;
     }
     // The exact peak: of the products that round to it, the largest in 64 bits.  It
@@ -419,14 +457,14 @@ __global__ void __launch_bounds__(THREADS) quant_rows_kernel(const __grid_consta
     while (near) {
         const int b = __ffs(near) - 1;
         near &= near - 1;
-        settle_code<DT>(a, row, at(b / VE) + b % VE, exact);
+        settle_code<DT, NORM && DT == LB_F32>(a, row, at(b / VE) + b % VE, exact);
     }
 }
 
 // Rows of more columns than a block's registers hold: one block per row, in 64
 // bits, the row read twice.  Bound by the 64-bit arithmetic and by loads of one
 // element: 4096 x 40000 fp32 715 to 730 us, 1.1 TB/s (17% of the copy rate).
-template <int DT>
+template <int DT, bool NORM>
 __global__ void __launch_bounds__(256) quant_wide_kernel(const __grid_constant__ QuantArgs a) {
     using X = Elem<DT>;
     __shared__ double red[32];
@@ -439,7 +477,7 @@ __global__ void __launch_bounds__(256) quant_wide_kernel(const __grid_constant__
         typename X::T* sum = static_cast<typename X::T*>(a.sum) + row * a.lds;
         for (int i = threadIdx.x; i < a.cols; i += 256) sum[i] = X::put(X::get(x[i]) + X::get(r[i]));
     }
-    quant_row_64<DT, false>(a, row, threadIdx.x, 256, red);
+    quant_row_64<DT, false, NORM && DT == LB_F32>(a, row, threadIdx.x, 256, red);
 }
 
 template <int DT, int C, bool ALIGNED, int THREADS, bool NORM>
@@ -476,7 +514,7 @@ cudaError_t launch_rows(const QuantArgs& a, cudaStream_t s) {
     if constexpr (!(NORM && kWide))
         if (a.cols <= 256 * 32) return launch_block<DT, 32 / VE, ALIGNED, 256, NORM>(a, s);
     if (a.cols <= kMaxThreads * 32) return launch_block<DT, 32 / VE, ALIGNED, kMaxThreads, NORM>(a, s);
-    return launch_dense(quant_wide_kernel<DT>, (unsigned)a.rows, 256, 0, 1, s, a);
+    return launch_dense(quant_wide_kernel<DT, NORM>, (unsigned)a.rows, 256, 0, 1, s, a);
 }
 
 lb_status quant_call(QuantArgs a, int dt, cudaStream_t s) {

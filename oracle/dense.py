@@ -10,13 +10,18 @@ def quantize(v, size=None):
     """(codes, scales) of the rows of v; size multiplies the scale (1 without a norm).
 
     Rows of zeros: codes 0, scale 0.  Rows with a NaN or an infinity: codes 0, scale NaN.
+    The quotients are formed in 64-bit significands: 127 v is exact there (60 bits at most),
+    so a tie stays one, and what is no tie is at least 2^-62 away, relatively, which the one
+    rounding (2^-64) does not bridge.
     """
+    assert np.finfo(np.longdouble).nmant >= 63, "needs a long double of 64 bits or more"
     v = np.asarray(v, dtype=np.float64)
     with np.errstate(all="ignore"):
         peak = np.max(np.abs(v), axis=1)
         fine = np.isfinite(peak) & (peak > 0)
         safe = np.where(fine, peak, 1.0)
-        q = np.rint(np.where(fine[:, None], v, 0.0) * 127.0 / safe[:, None])
+        q = np.rint(np.where(fine[:, None], v, 0.0).astype(np.longdouble) * 127
+                    / safe[:, None].astype(np.longdouble))
         scale = np.where(np.isfinite(peak), peak, np.nan) / 127.0
         if size is not None:
             scale = scale * size

@@ -1,8 +1,11 @@
 """Host side of the dense path, and the parts of its kernels that also run on the host (CPU)."""
-import os
 import subprocess
+from fractions import Fraction
+
+import numpy as np
 
 from binary_rank_linear_lb_b200 import build
+from oracle import dense
 
 # ------------------------------------------------------------ waits that give up
 # The tile loop of the 8-bit linear's draining warps against barriers with phases, the
@@ -116,3 +119,17 @@ def compile_and_run(tmp_path, program, name):
 def test_a_wait_that_gave_up_leaves_every_later_tile_unsummed(tmp_path):
     r = compile_and_run(tmp_path, DRAIN_PROGRAM, "drain")
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+# ------------------------------------------------------------ the oracle's codes at a tie
+def test_oracle_codes_of_ties_with_48_bit_products():
+    """v = (2 k + 1) peak / 254 exactly: code k or k + 1, whichever is even."""
+    rng = np.random.default_rng(3)
+    for m in range(1, 254, 2):
+        u, w0 = int(rng.integers(1 << 15, 66000)) | 1, int(rng.integers(1 << 23, 1 << 24)) | 1
+        s = np.array([[254 * u, m * u, -m * u, m * u + 1, m * u - 1]], dtype=np.float64) * 2.0 ** -20
+        w = np.full(5, w0 * 2.0 ** -30)
+        even = m // 2 + (m // 2) % 2
+        assert Fraction(s[0, 1] * w[1]) * 127 / Fraction(s[0, 0] * w[0]) == Fraction(m, 2)
+        q, _ = dense.rmsnorm_quantize(s, w)
+        assert q.tolist() == [[127, even, -even, m // 2 + 1, m // 2]], m

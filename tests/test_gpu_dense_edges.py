@@ -4,6 +4,7 @@ Bounds are those of test_gpu_dense (check_logprobs).
 """
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -45,3 +46,40 @@ def test_a_token_whose_scale_is_nan_through_the_chain():
     r = lb.Head(*lb.quantize_rows(w)).logprobs(h, random_tokens(3, 40, 3), top=32)
     assert torch.equal(r.top_id[1], torch.arange(32, device="cuda")) and r.top_logprob[1].isnan().all()
     assert r.top_logprob[[0, 2]].isfinite().all()
+
+
+# ------------------------------------------------------------ codes on a border, 48-bit products
+def exact_codes(s, w):
+    """rint(127 s w / max|s w|) of whole numbers, ties to even, in integers."""
+    v = [int(a) * int(b) for a, b in zip(s, w)]
+    peak = max(abs(a) for a in v)
+    out = []
+    for a in v:
+        k, rest = divmod(254 * abs(a) + peak, 2 * peak)       # floor(quotient + 1/2)
+        k -= rest == 0 and k % 2                              # a tie: the even one
+        out.append(k if a >= 0 else -k)
+    return out
+
+
+@pytest.mark.parametrize("cols", [7, 700, 5000, 40000])
+def test_ties_of_fp32_products(cols):
+    """v = (2 k + 1) peak / 254 exactly, with products of up to 48 bits: 127 v needs more
+    than the 53 bits of a double.  And products one 2^-48 beside such a tie."""
+    rng = np.random.default_rng(cols)
+    for m in range(1, 254, 2 if cols < 5000 else 14):
+        u = int(rng.integers(1 << 15, 66000)) | 1
+        w0 = m * u + 2 if m > 126 else int(rng.integers(1 << 23, 1 << 24)) | 1
+        s = np.zeros(cols, dtype=np.int64)
+        w = np.full(cols, w0, dtype=np.int64)
+        s[0] = 254 * u
+        s[1:4] = m * u, -m * u, m * u + 1
+        if m > 126:                                           # (m u + a)(w0 - a) = m u w0 + 2 a - a^2
+            s[4:6] = m * u + 1, m * u + 3
+            w[4:6] = w0 - 1, w0 - 3
+        s[6] = m * u
+        s[7:] = rng.integers(0, 127, max(cols - 7, 0)) * 2 * u   # (small: whole codes)
+        s[cols - 1] = m * u
+        x = torch.tensor(np.stack([s, -s]), dtype=F32, device="cuda") * 2.0 ** -24
+        q, _, _ = lb.rmsnorm_quantize(x, torch.tensor(w, dtype=F32, device="cuda") * 2.0 ** -23)
+        want = exact_codes(s, w)
+        assert q[0].tolist() == want and q[1].tolist() == [-c for c in want], m
