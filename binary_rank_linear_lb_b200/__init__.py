@@ -472,14 +472,19 @@ class Head:
     def logits(self, h: torch.Tensor, dtype: torch.dtype = torch.float32,
                stream=None) -> torch.Tensor:
         """Logits (tokens x vocab) of residual streams h (tokens x hidden, or one token's)."""
-        h2 = h if h.dim() == 2 else h.reshape(1, -1)
-        xq, xs, _ = rmsnorm_quantize(h2, self.norm_weight, eps=self.eps, stream=stream)
-        return linear_int8(xq, xs, self.wq, self.ws, dtype=dtype, stream=stream)
+        if stream is not None:
+            return _on_stream(stream, (h, self.wq, self.ws, self.norm_weight),
+                              lambda: self.logits(h, dtype))
+        xq, xs, _ = rmsnorm_quantize(h if h.dim() == 2 else h.reshape(1, -1), self.norm_weight, eps=self.eps)
+        return linear_int8(xq, xs, self.wq, self.ws, dtype=dtype)
 
     def logprobs(self, h: torch.Tensor, tokens: Optional[torch.Tensor] = None, top: int = 0,
                  stream=None) -> TokenLogprobs:
         """Log probabilities of ``tokens``, entropy and alternatives after h (see token_logprobs)."""
-        return token_logprobs(self.logits(h, stream=stream), tokens, top, stream)
+        if stream is not None:
+            return _on_stream(stream, (h, self.wq, self.ws, self.norm_weight, tokens),
+                              lambda: self.logprobs(h, tokens, top))
+        return token_logprobs(self.logits(h), tokens, top)
 
 
 # ------------------------------------------------------------------ stacks

@@ -83,3 +83,33 @@ def test_ties_of_fp32_products(cols):
         q, _, _ = lb.rmsnorm_quantize(x, torch.tensor(w, dtype=F32, device="cuda") * 2.0 ** -23)
         want = exact_codes(s, w)
         assert q[0].tolist() == want and q[1].tolist() == [-c for c in want], m
+
+
+# ------------------------------------------------------------ head: batches, streams, types
+def tiny_head(vocab=500, hidden=256, norm=True):
+    return lb.Head(*lb.quantize_rows(normal((vocab, hidden), 71)),
+                   normal((hidden,), 72, F16) if norm else None)
+
+
+def test_head_copies_what_it_reshapes_on_the_given_stream():
+    """A token that no view makes a row of, written on the stream that is given: read after
+    that, not before."""
+    head, side = tiny_head(), torch.cuda.Stream()
+    src, t = normal((64, 256, 64), 75), random_tokens(64 * 64, 500, 78)
+    slow = torch.empty(1 << 28, device="cuda")
+    for pick in (lambda h: h[3:4, :16, :16].transpose(1, 2),):
+        tokens = t[:1]
+        want = head.logprobs(pick(src).contiguous().view(-1, 256), tokens.reshape(-1), 3)
+        for call in (lambda h: (head.logits(h, stream=side),), lambda h: head.logprobs(h, tokens, 3, side)):
+            h = torch.zeros_like(src)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                for _ in range(20):
+                    slow.fill_(1.0)                   # some 3 ms before h is written
+                h.copy_(src)
+            got = call(pick(h))
+            side.synchronize()
+            if len(got) == 1:
+                got = lb.token_logprobs(got[0], tokens.reshape(-1), 3)
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
