@@ -469,21 +469,32 @@ class Head:
         self.wq, self.ws, self.norm_weight, self.eps = wq, ws, norm_weight, eps
         self.vocab, self.hidden = wq.shape
 
+    def _rows(self, h: torch.Tensor) -> torch.Tensor:
+        """h as a matrix of tokens (a copy where it is not one and not contiguous)."""
+        one = h.dim() != 2 and h.numel() == self.hidden
+        if not one and (h.dim() < 2 or h.shape[-1] != self.hidden):
+            raise ValueError(f"h must have {self.hidden} columns, got shape {tuple(h.shape)}")
+        return h if h.dim() == 2 else h.contiguous().view(-1, self.hidden)
+
     def logits(self, h: torch.Tensor, dtype: torch.dtype = torch.float32,
                stream=None) -> torch.Tensor:
-        """Logits (tokens x vocab) of residual streams h (tokens x hidden, or one token's)."""
+        """Logits (tokens x vocab) of residual streams h: tokens x hidden, one token's, or a
+        batch (... x hidden), whose tokens follow one another in order."""
         if stream is not None:
             return _on_stream(stream, (h, self.wq, self.ws, self.norm_weight),
                               lambda: self.logits(h, dtype))
-        xq, xs, _ = rmsnorm_quantize(h if h.dim() == 2 else h.reshape(1, -1), self.norm_weight, eps=self.eps)
+        xq, xs, _ = rmsnorm_quantize(self._rows(h), self.norm_weight, eps=self.eps)
         return linear_int8(xq, xs, self.wq, self.ws, dtype=dtype)
 
     def logprobs(self, h: torch.Tensor, tokens: Optional[torch.Tensor] = None, top: int = 0,
                  stream=None) -> TokenLogprobs:
-        """Log probabilities of ``tokens``, entropy and alternatives after h (see token_logprobs)."""
+        """Log probabilities of ``tokens`` (one per token of h, in any shape), entropy and
+        alternatives after h (see token_logprobs)."""
         if stream is not None:
             return _on_stream(stream, (h, self.wq, self.ws, self.norm_weight, tokens),
                               lambda: self.logprobs(h, tokens, top))
+        if tokens is not None and tokens.dim() != 1:
+            tokens = tokens.reshape(-1)
         return token_logprobs(self.logits(h), tokens, top)
 
 

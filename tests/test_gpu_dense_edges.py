@@ -91,14 +91,32 @@ def tiny_head(vocab=500, hidden=256, norm=True):
                    normal((hidden,), 72, F16) if norm else None)
 
 
+@pytest.mark.parametrize("norm", [True, False])
+def test_head_of_a_batch_of_sequences(norm):
+    """(batch, sequence, hidden) streams are batch * sequence tokens, in order."""
+    head, h = tiny_head(norm=norm), normal((3, 5, 256), 73)
+    t = random_tokens(15, 500, 74)
+    want = head.logits(h.reshape(15, 256))
+    assert torch.equal(head.logits(h), want) and want.shape == (15, 500)
+    assert torch.equal(head.logits(h.transpose(0, 1)), head.logits(h.transpose(0, 1).reshape(15, 256)))
+    for a, b in zip(head.logprobs(h, t.view(3, 5), 4), head.logprobs(h.reshape(15, 256), t, 4)):
+        assert torch.equal(a, b)
+    # one token in any shape, as ever
+    assert torch.equal(head.logits(h[0, 0]), head.logits(h[0, :1]))
+    assert torch.equal(head.logits(h[0, 0].view(1, 4, 64)), head.logits(h[0, :1]))
+    for bad in (normal((2, 512), 1), normal((2, 3, 128), 1), normal((512,), 1), normal((3, 4, 1), 1)):
+        with pytest.raises(ValueError):
+            head.logits(bad)
+
+
 def test_head_copies_what_it_reshapes_on_the_given_stream():
-    """A token that no view makes a row of, written on the stream that is given: read after
-    that, not before."""
+    """A strided token or batch, written on the stream that is given: read after that, not
+    before."""
     head, side = tiny_head(), torch.cuda.Stream()
     src, t = normal((64, 256, 64), 75), random_tokens(64 * 64, 500, 78)
     slow = torch.empty(1 << 28, device="cuda")
-    for pick in (lambda h: h[3:4, :16, :16].transpose(1, 2),):
-        tokens = t[:1]
+    for pick in (lambda h: h[3:4, :16, :16].transpose(1, 2), lambda h: h[3, :, 5], lambda h: h.transpose(1, 2)):
+        tokens = t[:1] if pick(src).numel() == 256 else t.view(64, 64).t()
         want = head.logprobs(pick(src).contiguous().view(-1, 256), tokens.reshape(-1), 3)
         for call in (lambda h: (head.logits(h, stream=side),), lambda h: head.logprobs(h, tokens, 3, side)):
             h = torch.zeros_like(src)
