@@ -487,15 +487,15 @@ class Head:
         return linear_int8(xq, xs, self.wq, self.ws, dtype=dtype)
 
     def logprobs(self, h: torch.Tensor, tokens: Optional[torch.Tensor] = None, top: int = 0,
-                 stream=None) -> TokenLogprobs:
+                 stream=None, dtype: torch.dtype = torch.float32) -> TokenLogprobs:
         """Log probabilities of ``tokens`` (one per token of h, in any shape), entropy and
-        alternatives after h (see token_logprobs)."""
+        alternatives after h (see token_logprobs), of logits that are held in ``dtype``."""
         if stream is not None:
             return _on_stream(stream, (h, self.wq, self.ws, self.norm_weight, tokens),
-                              lambda: self.logprobs(h, tokens, top))
+                              lambda: self.logprobs(h, tokens, top, dtype=dtype))
         if tokens is not None and tokens.dim() != 1:
             tokens = tokens.reshape(-1)
-        return token_logprobs(self.logits(h), tokens, top)
+        return token_logprobs(self.logits(h, dtype), tokens, top)
 
 
 # ------------------------------------------------------------------ stacks

@@ -131,3 +131,13 @@ def test_head_copies_what_it_reshapes_on_the_given_stream():
                 got = lb.token_logprobs(got[0], tokens.reshape(-1), 3)
             for a, b in zip(got, want):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_head_logprobs_of_logits_of_a_type(dtype):
+    head, h, t = tiny_head(), normal((9, 256), 76), random_tokens(9, 500, 77)
+    x = head.logits(h, dtype=dtype)
+    r = head.logprobs(h, t, 5, dtype=dtype)
+    check_logprobs(r, x, t, 5, dtype)
+    for a, b in zip(r, lb.token_logprobs(x, t, 5)):
+        assert torch.equal(a, b)
