@@ -113,19 +113,28 @@ inline bool dtype_ok(int t) { return t == LB_F16 || t == LB_BF16 || t == LB_F32;
 inline size_t dtype_size(int t) { return t == LB_F32 ? 4 : 2; }
 inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// The status of a call whose last runtime call returned e.  An error is reported here,
+// so it is taken back from the runtime: other entry points ask that for their own.
+inline lb_status dense_status(cudaError_t e) {
+    if (e == cudaSuccess) return LB_OK;
+    (void)cudaGetLastError();
+    return LB_ERR_CUDA;
+}
+
 // LB_OK when the current device is an sm_100 part; its SM count.  (Asked once per
 // device: two runtime calls are a tenth of a small call's time on the host.)
 inline lb_status dense_device(int& sms) {
     constexpr int kDevices = 64;
     static std::atomic<int> known[kDevices];       // 0: not asked yet, -1: another part, else its SMs
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return LB_ERR_CUDA;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kDevices) return e == cudaSuccess ? LB_ERR_CUDA : dense_status(e);
     sms = known[dev].load(std::memory_order_relaxed);
     if (sms == 0) {
         int major = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return LB_ERR_CUDA;
+        cudaError_t a = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+        if (a == cudaSuccess) a = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (a != cudaSuccess) return dense_status(a);
         if (major != 10) sms = -1;
         known[dev].store(sms, std::memory_order_relaxed);
     }

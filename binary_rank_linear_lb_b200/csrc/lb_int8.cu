@@ -811,7 +811,7 @@ Encode encoder() {
     static const Encode fn = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+        if (dense_status(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r)) != LB_OK ||
             r != cudaDriverEntryPointSuccess)
             f = nullptr;
         return reinterpret_cast<Encode>(f);
@@ -939,7 +939,7 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
     if (mma_ok(a)) {
         if (M == 1) {
             const cudaError_t e = with_dtype(y_dtype, [&](auto d) { return launch_one<d.value>(a, sms, s); });
-            return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+            return dense_status(e);
         }
         const MmaPlan p = mma_plan(M, out, in, sms);
         CUtensorMap wm, xm;
@@ -957,12 +957,12 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
             return p.lg_split > 0 ? launch_mma<d.value, true, 2>(a, p, wm, xm, sms, s)
                                   : launch_mma<d.value, false, 2>(a, p, wm, xm, sms, s);
         });
-        return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+        return dense_status(e);
     }
     const cudaError_t e = with_dtype(y_dtype, [&](auto d) {
         return M <= 16   ? launch_general<d.value, 1>(a, s)
                : M <= 32 ? launch_general<d.value, 2>(a, s)
                          : launch_general<d.value, 4>(a, s);
     });
-    return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+    return dense_status(e);
 }

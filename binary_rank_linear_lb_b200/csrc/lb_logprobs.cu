@@ -587,5 +587,5 @@ extern "C" lb_status lb_token_logprobs(const void* logits, lb_dtype dtype, int64
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
         with_dtype(dtype, [&](auto d) { return launch_logprobs<d.value>(a, rows, sms, s); });
-    return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+    return dense_status(e);
 }

@@ -532,7 +532,7 @@ lb_status quant_call(QuantArgs a, int dt, cudaStream_t s) {
         if (a.norm) return aligned ? launch_rows<d.value, true, true>(a, s) : launch_rows<d.value, false, true>(a, s);
         return aligned ? launch_rows<d.value, true, false>(a, s) : launch_rows<d.value, false, false>(a, s);
     });
-    return e == cudaSuccess ? LB_OK : LB_ERR_CUDA;
+    return dense_status(e);
 }
 
 bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {

@@ -2,6 +2,7 @@
 
 Bounds are those of test_gpu_dense (check_logprobs).
 """
+import ctypes
 import math
 
 import numpy as np
@@ -141,3 +142,38 @@ def test_head_logprobs_of_logits_of_a_type(dtype):
     check_logprobs(r, x, t, 5, dtype)
     for a, b in zip(r, lb.token_logprobs(x, t, 5)):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------ a refused launch leaves no trace
+def test_a_refused_launch_is_not_reported_by_the_next_call():
+    """While a blocking stream is captured, CUDA refuses launches on the legacy stream with an
+    error code.  The call returns it; calls after it do not."""
+    rt = ctypes.CDLL("libcudart.so.12")               # (the one torch has loaded)
+    x, latent = normal((4, 64), 1), normal((64, 64), 2)
+    q, scale = torch.empty((4, 64), dtype=torch.int8, device="cuda"), torch.empty(4, device="cuda")
+    words = lb.pack_signs(latent, axis=1)
+    y, t = normal((4, 64), 3), torch.zeros(4, dtype=torch.int64, device="cuda")
+    ent, out = torch.empty(4, device="cuda"), torch.empty((4, 4), device="cuda")
+    L, p = lb.lib(), lambda a: a.data_ptr()
+    calls = [
+        lambda: L.lb_quantize_rows(p(x), lb.LB_F32, 4, 64, 64, p(q), 64, p(scale), None),
+        lambda: L.lb_linear_int8(p(q), 64, p(scale), 4, p(q), 64, p(scale), 64, 4, p(out), lb.LB_F32, 4, None),
+        lambda: L.lb_linear_int8(p(q), 64, p(scale), 1, p(q), 64, p(scale), 64, 4, p(out), lb.LB_F32, 4, None),
+        lambda: L.lb_linear_int8(p(q) + 1, 65, p(scale), 3, p(q) + 1, 65, p(scale), 63, 3, p(out), lb.LB_F32, 4,
+                                 None),
+        lambda: L.lb_token_logprobs(p(y), lb.LB_F32, 4, 64, 64, None, None, p(ent), 0, None, None, None)]
+    for call in calls:
+        assert call() == lb.LB_OK
+    for call in calls:
+        torch.cuda.synchronize()
+        s, g = ctypes.c_void_p(), ctypes.c_void_p()
+        assert rt.cudaStreamCreate(ctypes.byref(s)) == 0
+        assert rt.cudaStreamBeginCapture(s, 0) == 0   # global: other streams' unsafe calls fail
+        try:
+            status = call()
+        finally:
+            rt.cudaStreamEndCapture(s, ctypes.byref(g))   # (invalidated: no graph)
+            rt.cudaGetLastError()                     # torch's own runtime is left as it was
+            rt.cudaStreamDestroy(s)
+        assert status == lb.LB_ERR_CUDA
+        assert torch.equal(lb.pack_signs(latent, axis=1), words)
