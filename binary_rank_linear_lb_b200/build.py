@@ -5,16 +5,21 @@
 Compiles every ``csrc/*.cu`` with nvcc for ``sm_100a`` only and links them into
 ``binary_rank_linear_lb_b200/liblb.so``, and ``csrc/lb_torch.cpp`` (the dense path's argument
 marshalling for torch tensors) with g++ into ``lb_torch.so`` beside it.  Runs without a GPU
-(nvcc cross-compiles).
+(nvcc cross-compiles).  Where g++, torch or Python's headers are missing, liblb.so is built
+alone, with a warning: its C ABI needs none of them.  (Without torch the package cannot be
+imported; run this file by its path.)
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -56,6 +61,17 @@ def up_to_date() -> bool:
     return newer(LIB, deps()) and newer(EXT, ext_deps())
 
 
+def ext_lacks() -> Optional[str]:
+    """What is missing to build lb_torch.so, or None."""
+    if shutil.which("g++") is None:
+        return "no g++"
+    if importlib.util.find_spec("torch") is None:
+        return "no torch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "no Python headers"
+    return None
+
+
 def build_ext() -> None:
     """lb_torch.so, linked against the liblb.so beside it and the installed torch."""
     import torch
@@ -79,7 +95,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     if force or not newer(LIB, deps()):
         build_lib(verbose)
-    build_ext()
+    lacks = ext_lacks()
+    if lacks is None:
+        build_ext()
+    else:
+        if os.path.exists(EXT) and not newer(EXT, ext_deps()):     # of other sources: better none
+            os.remove(EXT)
+        warnings.warn(f"lb_torch.so is not built ({lacks}): liblb.so is complete, the dense "
+                      "path's Python functions will raise")
     return LIB
 
 

@@ -1,8 +1,10 @@
 """Host side of the dense path, and the parts of its kernels that also run on the host (CPU)."""
+import os
 import subprocess
 from fractions import Fraction
 
 import numpy as np
+import pytest
 
 from binary_rank_linear_lb_b200 import build
 from oracle import dense
@@ -133,3 +135,17 @@ def test_oracle_codes_of_ties_with_48_bit_products():
         assert Fraction(s[0, 1] * w[1]) * 127 / Fraction(s[0, 0] * w[0]) == Fraction(m, 2)
         q, _ = dense.rmsnorm_quantize(s, w)
         assert q.tolist() == [[127, even, -even, m // 2 + 1, m // 2]], m
+
+
+# ------------------------------------------------------------ building
+def test_the_c_library_is_built_where_the_torch_binding_cannot_be(tmp_path, monkeypatch):
+    """No g++: liblb.so stands, a binding of other sources goes, and the caller is told."""
+    build.build()
+    stale = tmp_path / "lb_torch.so"
+    stale.write_bytes(b"")
+    os.utime(stale, (1, 1))
+    monkeypatch.setattr(build, "EXT", str(stale))
+    monkeypatch.setenv("PATH", str(tmp_path))
+    with pytest.warns(UserWarning, match="lb_torch.so.*g\\+\\+"):
+        assert build.build() == build.LIB
+    assert not stale.exists()
