@@ -12,6 +12,7 @@ imported; run this file by its path.)
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -26,6 +27,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblb.so")
 EXT = os.path.join(PKG, "lb_torch.so")
+STAMP = os.path.join(PKG, "_build", "lb_torch.made_for")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -57,8 +59,25 @@ def newer(target, sources_) -> bool:
     return all(os.path.getmtime(p) <= t for p in sources_)
 
 
+def made_for() -> str:
+    """What lb_torch.so fits: the installed torch and this Python (neither shows in the times
+    of its sources)."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "none"
+    return f"torch {torch} {sysconfig.get_config_var('SOABI')}\n"
+
+
+def ext_current() -> bool:
+    if not newer(EXT, ext_deps()) or not os.path.exists(STAMP):
+        return False
+    with open(STAMP) as f:
+        return f.read() == made_for()
+
+
 def up_to_date() -> bool:
-    return newer(LIB, deps()) and newer(EXT, ext_deps())
+    return newer(LIB, deps()) and ext_current()
 
 
 def ext_lacks() -> Optional[str]:
@@ -73,6 +92,16 @@ def ext_lacks() -> Optional[str]:
 
 
 def build_ext() -> None:
+    """lb_torch.so, and beside the objects what it was made for."""
+    if os.path.exists(STAMP):
+        os.remove(STAMP)
+    compile_ext()
+    os.makedirs(os.path.dirname(STAMP), exist_ok=True)
+    with open(STAMP, "w") as f:
+        f.write(made_for())
+
+
+def compile_ext() -> None:
     """lb_torch.so, linked against the liblb.so beside it and the installed torch."""
     import torch
     base = os.path.dirname(torch.__file__)
@@ -99,7 +128,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if lacks is None:
         build_ext()
     else:
-        if os.path.exists(EXT) and not newer(EXT, ext_deps()):     # of other sources: better none
+        if os.path.exists(EXT) and not ext_current():      # of other sources: better none
             os.remove(EXT)
         warnings.warn(f"lb_torch.so is not built ({lacks}): liblb.so is complete, the dense "
                       "path's Python functions will raise")

@@ -149,3 +149,19 @@ def test_the_c_library_is_built_where_the_torch_binding_cannot_be(tmp_path, monk
     with pytest.warns(UserWarning, match="lb_torch.so.*g\\+\\+"):
         assert build.build() == build.LIB
     assert not stale.exists()
+
+
+def test_the_binding_is_built_again_for_another_torch_or_python(tmp_path, monkeypatch):
+    build.build()
+    assert build.up_to_date()
+    built = []
+    monkeypatch.setattr(build, "STAMP", str(tmp_path / "stamp"))
+    monkeypatch.setattr(build, "compile_ext", lambda: built.append(1))
+    for made_for in (None, "torch 0.1 cpython-27\n"):      # an older tree's build, another torch's
+        if made_for is not None:
+            (tmp_path / "stamp").write_text(made_for)
+        assert not build.up_to_date()
+        build.build()
+        assert built.pop() and build.up_to_date()
+        build.build()
+        assert not built
