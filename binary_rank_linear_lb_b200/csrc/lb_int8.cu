@@ -943,10 +943,9 @@ extern "C" lb_status lb_linear_int8(const int8_t* xq, int64_t ldx, const float* 
         }
         const MmaPlan p = mma_plan(M, out, in, sms);
         CUtensorMap wm, xm;
-        // (the pitch of a single row is never used; the map wants a multiple of 16)
+        // (the pitch of a single channel is never used; the map wants a multiple of 16)
         if (!code_map(&wm, wq, out, in, out == 1 ? (in + 15) / 16 * 16 : ldw, kTileCh) ||
-            !code_map(&xm, xq, M, in, M == 1 ? (in + 15) / 16 * 16 : ldx,
-                      p.pair ? p.nt / 2 : p.nt))
+            !code_map(&xm, xq, M, in, ldx, p.pair ? p.nt / 2 : p.nt))
             return LB_ERR_CUDA;
         const cudaError_t e = with_dtype(y_dtype, [&](auto d) {
             if (p.pair && p.kper == 1) return launch_pair<d.value, 1>(a, p, wm, xm, sms, s);
