@@ -1,16 +1,22 @@
 """Edges of the dense path on the GPU, each against the 64-bit oracle or exact arithmetic.
 
-Bounds are those of test_gpu_dense (check_logprobs).
+Bounds are those of test_gpu_dense (check_codes, check_linear, check_logprobs).
 """
 import ctypes
 import math
+import os
+import subprocess
+import sys
+import threading
 
 import numpy as np
 import pytest
 import torch
 
 import binary_rank_linear_lb_b200 as lb
-from test_gpu_dense import BF16, F16, F32, check_logprobs, normal, random_tokens
+from oracle import dense
+from test_gpu_dense import (BF16, F16, F32, check_codes, check_linear, check_logprobs, codes, f64, normal, pitched,
+                            random_tokens, scales)
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +183,127 @@ def test_a_refused_launch_is_not_reported_by_the_next_call():
             rt.cudaStreamDestroy(s)
         assert status == lb.LB_ERR_CUDA
         assert torch.equal(lb.pack_signs(latent, axis=1), words)
+
+
+# ------------------------------------------------------------ the ends of the ranges
+def test_the_widest_rows():
+    """2^24 columns: quantised, and scored with 32 alternatives."""
+    n = 1 << 24
+    x = normal((2, n), 81)
+    check_codes(*lb.quantize_rows(x), dense.quantize(f64(x)), "2^24")
+    t = random_tokens(2, n, 82)
+    check_logprobs(lb.token_logprobs(x, t, 32), x, t, 32, "2^24")
+
+
+@pytest.mark.parametrize("M,k,n", [(1 << 20, 16, 3), (3, 16, 1 << 20), (1, 32, (1 << 20) + 1), (1 << 20, 16, 1),
+                                   (1 << 18, 17, 5), (300, 131071, 260)])
+def test_linear_of_many_tokens_or_channels(M, k, n):
+    xq, wq = pitched(codes(M, k, 1), k if k == 17 else None), pitched(codes(n, k, 2), k if k == 17 else None)
+    xs, ws = scales(M, 3), scales(n, 4)
+    check_linear(lb.linear_int8(xq, xs, wq, ws), xq, xs, wq, ws, (M, k, n))
+
+
+@pytest.mark.parametrize("M,k", [(1, 17), (2, 17), (5, 129), (300, 4097)])
+def test_linear_of_one_channel_of_any_length(M, k):
+    """A single channel's pitch is its length, off 16 bytes or not."""
+    xq, wq = pitched(codes(M, k, 1)), codes(1, k, 2)
+    xs, ws = scales(M, 3), scales(1, 4)
+    check_linear(lb.linear_int8(xq, xs, wq, ws), xq, xs, wq, ws, (M, k))
+
+
+def test_many_short_rows():
+    x = normal((1 << 20, 5), 83, BF16)
+    check_codes(*lb.quantize_rows(x), dense.quantize(f64(x)), "rows")
+    t = random_tokens(1 << 17, 5, 84)
+    check_logprobs(lb.token_logprobs(x[:1 << 17], t, 5), x[:1 << 17], t, 5, "rows")
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing has been loaded or asked for yet when the calls are captured."""
+    code = '''
+import torch, binary_rank_linear_lb_b200 as lb
+h = torch.randn(24, 512, device="cuda")
+w = torch.randint(-127, 128, (3000, 512), device="cuda").to(torch.int8)
+ws, t = torch.rand(3000, device="cuda"), torch.zeros(24, dtype=torch.int64, device="cuda")
+head, g = lb.Head(w, ws), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    r = head.logprobs(h, t, 5)
+    one = head.logits(h[0])
+g.replay()
+torch.cuda.synchronize()
+for a, b in zip(r, head.logprobs(h, t, 5)):
+    assert torch.equal(a, b)
+assert torch.equal(one, head.logits(h[0]))
+print("done")
+'''
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
+
+
+def test_calls_of_several_threads_at_once():
+    head, hs = tiny_head(), [normal((7 + i, 256), 90 + i) for i in range(4)]
+    want = [head.logprobs(h, top=4) for h in hs]
+    torch.cuda.synchronize()
+    got = [[] for _ in hs]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.default_stream())
+        for _ in range(50):
+            got[i].append(head.logprobs(hs[i], top=4, stream=s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    for a, b in zip(want, got):
+        assert len(b) == 50
+        for r in b:
+            assert all(torch.equal(u, v) for u, v in zip(a[1:], r[1:]))
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("cols", [5, 333, 777, 5001, 8192, 34567])
+def test_one_buffer_as_x_residual_and_sum(dtype, cols):
+    x, w = normal((5, cols), 95, dtype), normal((cols,), 96, F16)
+    want = (x.double() * 2).to(dtype)
+    q, s, total = lb.rmsnorm_quantize(x, w, x, sum_out=x)
+    assert total is x and torch.equal(x, want)
+    check_codes(q, s, dense.rmsnorm_quantize(f64(want), f64(w)), cols)
+
+
+def test_default_stream_by_handle_and_from_a_side_stream():
+    head, h, side = tiny_head(), normal((6, 256), 97), torch.cuda.Stream()
+    want = head.logprobs(h, top=3)
+    torch.cuda.synchronize()
+    for arg in (0, torch.cuda.default_stream()):
+        for here in (torch.cuda.default_stream(), side):
+            with torch.cuda.stream(here):
+                got = head.logprobs(h, top=3, stream=arg)
+            torch.cuda.synchronize()
+            for a, b in zip(got[1:], want[1:]):
+                assert torch.equal(a, b)
+
+
+def test_captured_with_a_stream_argument_that_is_joined():
+    head, h, side = tiny_head(), normal((6, 256), 98), torch.cuda.Stream()
+    head.logprobs(h, top=3)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        h2 = h * 2
+        side.wait_stream(main)
+        r = head.logprobs(h2, top=3, stream=side)
+        main.wait_stream(side)
+        out = [t.clone() for t in r[1:]]
+    for seed in (1, 2):
+        h.copy_(normal((6, 256), seed))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, head.logprobs(h * 2, top=3)[1:]):
+            assert torch.equal(a, b)
