@@ -282,7 +282,9 @@ int lb_linear_path(int64_t M, int64_t in, int64_t out, int64_t r);
  *     by narrower loads, with the same results;
  *   - no workspace: a call keeps nothing, so calls on several streams, and
  *     captured graphs that are replayed together, share nothing;
- *   - bytes between the columns and the pitch are neither read nor written;
+ *   - bytes between the columns and the pitch are not written and change no result.  They
+ *     are not read either, but for lb_linear_int8 off 16 bytes: it reads aligned words of
+ *     4 bytes, so up to three bytes on either side of a row, and ignores those;
  *   - outputs overlap neither inputs nor one another, except where stated;
  *   - sizes of zero are refused (LB_ERR_INVALID_ARG).
  */
@@ -294,9 +296,11 @@ int lb_linear_path(int64_t M, int64_t in, int64_t out, int64_t r);
  *            of the row, q_i = rint(127 x_i / peak) of the exact quotient, ties to
  *            even, so -127 <= q_i <= 127
  *   scale  : device fp32 [rows], written: peak / 127
- * scale * q_i is within half a step of x_i.  A row of zeros has scale 0.  A row
- * with a NaN or an infinity has scale NaN and codes 0, so that what is computed
- * from it is NaN.  Errors: LB_ERR_INVALID_ARG (null pointer, rows or cols <= 0,
+ * scale * q_i is within half a step of x_i, as far as fp32 holds the scale: one
+ * below its normal range is rounded to its smallest steps (in the end to 0), one
+ * above its range (only a norm can give that) is an infinity.  A row of zeros has
+ * scale 0.  A row with a NaN or an infinity has scale NaN and codes 0, so that what
+ * is computed from it is NaN.  Errors: LB_ERR_INVALID_ARG (null pointer, rows or cols <= 0,
  * rows > 2^31 - 1, cols > 2^24, a pitch below cols or above 2^40, bad dtype),
  * LB_ERR_ALIGNMENT, LB_ERR_UNSUPPORTED, LB_ERR_CUDA.
  */
@@ -336,7 +340,7 @@ lb_status lb_rmsnorm_quantize(const void *x, lb_dtype x_dtype, int64_t rows, int
  * and then to y_dtype.  -128 is an ordinary code.  A device-side wait that gives
  * up (about 2 s) leaves NaN in the outputs it held up.  The fast kernels read xq
  * and wq in 16-byte pieces (pointers and pitches multiples of 16); other calls
- * run one that is tens of times slower for many tokens.
+ * run one that is some 10 times slower for few tokens and 20 to 40 times for many.
  * Errors: LB_ERR_INVALID_ARG (null pointer, M, in or out <= 0, M or out > 2^24,
  * M * out > 2^40, in > 131071 (the sum has to fit 32 bits), a pitch below its
  * columns or above 2^32, bad dtype), LB_ERR_ALIGNMENT, LB_ERR_UNSUPPORTED, LB_ERR_CUDA.

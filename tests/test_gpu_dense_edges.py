@@ -307,3 +307,20 @@ def test_captured_with_a_stream_argument_that_is_joined():
         torch.cuda.synchronize()
         for a, b in zip(out, head.logprobs(h * 2, top=3)[1:]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scales_past_the_range_of_fp32(dtype):
+    """A norm of one value among 65536 is 256 times its weight; a row's peak can be fp32's
+    smallest step."""
+    x = torch.zeros((2, 65536), dtype=dtype, device="cuda")
+    x[0, 5] = x[1, 9] = 1.0
+    w = torch.ones(65536, device="cuda")
+    w[5] = 3e38
+    q, s, _ = lb.rmsnorm_quantize(x, w, eps=0.0)
+    assert s[0] == math.inf and abs(float(s[1]) / (256 / 127) - 1) < 1e-6
+    assert q[0, 5] == q[1, 9] == 127 and q.count_nonzero() == 2
+    x = torch.zeros((1, 300), dtype=F32, device="cuda")
+    x[0, 7] = 2.0 ** -149
+    q, s = lb.quantize_rows(x)
+    assert s[0] == 0 and q[0, 7] == 127 and q.count_nonzero() == 1
