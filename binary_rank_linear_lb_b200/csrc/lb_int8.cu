@@ -29,7 +29,7 @@ struct Int8Args {
 // What bounds it: latency of a stage's loads with few blocks, reads of shared memory
 // with many; two words are loaded for each one used.  4097 -> 32000, one token: 140 us
 // (0.9 TB/s; rows on 16 bytes 21); 4097 -> 4096, 64 tokens 98 us, 512 tokens 256 us
-// (67 TOP/s).  Byte by byte these were 500, 216 and 485 us.
+// (67 TOP/s; 12 on 16 bytes).  Byte by byte these were 500, 216 and 485 us.
 constexpr int kGenTile = 64;
 constexpr int kGenPitch = 17;                // words of a staged row (16 used), odd: no bank conflicts
 
@@ -240,17 +240,18 @@ cudaError_t launch_one(const Int8Args& a, int sms, cudaStream_t s) {
 // zeros past the edges), warp 9 owns TMEM and issues the MMAs.  Two accumulators:
 // one tile is drained while the next is summed.
 //
-// What bounds it: HBM while the tokens are few (16 x 8192 -> 28672 bf16: 40.4 us, 5.8
-// TB/s, 90% of the copy rate), then what L2 gives an SM (see mma_plan), then the
-// MMAs and the card's power limit (4096 x 8192 -> 32000, pairs of CTAs: 672 us, 3190
-// TOP/s in a burst, 95% of twice the bf16 burst rate; some 770 us when it runs on).
+// What bounds it: HBM while the tokens are few (16 x 8192 -> 28672 bf16: 42.1 us a call,
+// 5.6 TB/s, 87% of the copy rate; 39.5 us, 93%, in a graph), then what L2 gives an SM (see
+// mma_plan), then the MMAs and the card's power limit (4096 x 8192 -> 32000, pairs of
+// CTAs: 675 us, 3180 TOP/s in a burst, 94% of twice the bf16 burst rate; 780 to 800 us
+// when it runs on).
 //
 // With few tiles the K blocks of a tile are split over a cluster of CTAs, which
 // exchange their partial sums through distributed shared memory (each CTA folds
 // and stores its share of the tokens).  Integer sums: the order does not matter.
 //
 // Every wait is bounded (about 2 s).  A CTA that gives up stores NaN for the
-// tiles it could not finish, frees its TMEM and returns.
+// tiles it could not finish and all after them, frees its TMEM and returns.
 constexpr int kMmaThreads = 320;
 constexpr int kDrainWarps = 8;
 constexpr int kLoadWarp = 8;
